@@ -1,6 +1,7 @@
 /*
  * w4.h -- C ABI of libw4.so: the group-wise INT4 weight-only quantized linear layer on MI355X
- * (gfx950).
+ * (gfx950), and the operators of a decoder layer around it (rotary positions, attention over a
+ * paged key-value cache, the residual norm).
  *
  *   y = x . W_hat^T (+ b),   W_hat[j][k] = s[j][G] * (code[j][k] - z[j][G]),  G = k / group_size
  *
@@ -319,6 +320,155 @@ int w4a8_linear(const uint16_t *x, int64_t M, int64_t ldx, const uint8_t *qweigh
 int w4a8_gemm(const int8_t *q, const float *s_x, int64_t M, int64_t ldq, const uint8_t *qweight,
               const uint16_t *s_w, const uint16_t *bias, int64_t d_out, int64_t d_in, void *y,
               int64_t ldy, int out_dtype, int32_t *acc, void *stream);
+
+/*
+ * The operators of a decoder layer that stand between its linears: rotary positions and the append
+ * to a paged key-value cache, attention of one new token and of prompts over that cache, and the
+ * residual norm.  (Lab5 基础: the layer's attention with its sliding window; Infra 第四部分: the
+ * paged cache of a serving batch.)
+ *
+ * w4_kv_cache -- a paged key-value cache and the sequences in it.  The struct is read on the host
+ * during the call; its arrays are device memory.
+ *   k, v        bf16, 16-byte aligned; element d of key-value head h in slot s of page p is
+ *               k[p * page_stride + s * slot_stride + h * head_stride + d]  (v likewise), so both
+ *               [page][slot][head][d] and [page][head][slot][d] fit.  Strides are in elements and
+ *               multiples of 8; what lies between two rows is never touched.
+ *   n_pages     pages in k and v (1 .. 2^31 - 1); page offsets may pass 32 bits, while the
+ *               elements spanned inside one page must be fewer than 2^31
+ *   page_size   slots of a page, a power of two, 1 .. 32768
+ *   n_kv_heads  1 .. 1024;   head_dim  a multiple of 8, 8 .. 256
+ *   page_table  int32 [n_seqs][ld_table], table_cols entries used: position p of sequence b lives
+ *               in slot p % page_size of page page_table[b][p / page_size].  Only entries of
+ *               positions that an operator reads or writes matter; the others may hold anything.
+ *               An entry outside [0, n_pages) never makes an access leave the cache (reads see
+ *               another page's values, appends are dropped).
+ *   kv_len      int32 [n_seqs]: keys of each sequence, the tokens of this call included.  Values
+ *               below 0 count as 0, values above table_cols * page_size as that.
+ * Slots that hold no visible key are never used, whatever bits they hold (NaN included).
+ *
+ * Token rows: sequence b has the rows q_start[b] <= t < q_start[b + 1] (q_start int32
+ * [n_seqs + 1], nondecreasing, q_start[0] = 0, q_start[n_seqs] = T), which are its LAST tokens: row
+ * q_start[b] + i stands at position kv_len[b] - (q_start[b + 1] - q_start[b]) + i.  A row whose
+ * position is negative sees no key and is not appended.
+ *
+ * Visible keys of a token at position p:  j <= p, and with window > 0 also
+ *   j > p - window  or  j < sinks    (the window counts the token itself; sinks are the first
+ *   tokens of a sequence that stay visible).  window = 0 means no window; sinks are then ignored.
+ */
+typedef struct w4_kv_cache {
+    uint16_t *k, *v;
+    int64_t n_pages, page_stride, slot_stride, head_stride;
+    int32_t page_size, n_kv_heads, head_dim;
+    const int32_t *page_table;
+    int64_t n_seqs, table_cols, ld_table;
+    const int32_t *kv_len;
+} w4_kv_cache;
+
+#define W4_MAX_HEAD_DIM 256
+#define W4_MAX_HEADS 1024           /* n_heads, n_kv_heads                                  */
+#define W4_NORM_MAX_D ((int64_t)1 << 15) /* the residual norm keeps a row in registers      */
+
+enum { W4_ROPE_HALF = 0, W4_ROPE_INTERLEAVED = 1 }; /* pairs (i, i + R/2), or (2i, 2i + 1)   */
+enum { W4_ROPE_PLAIN = 0, W4_ROPE_LINEAR = 1, W4_ROPE_NTK = 2, W4_ROPE_YARN = 3 };
+
+/*
+ * w4_rope_frequencies -- host-only: the angle per position of each rotated pair, and the amplitude,
+ * for the usual ways of reaching contexts longer than a model was trained on.  R = rot_dim (even,
+ * 2 .. 256), i < R / 2, plain frequencies f_i = base^(-2 i / R):
+ *   W4_ROPE_PLAIN   f_i                                       (factor and context are ignored)
+ *   W4_ROPE_LINEAR  f_i / factor                              (position interpolation)
+ *   W4_ROPE_NTK     f_i with base * factor^(R / (R - 2)): the lowest frequency is divided by
+ *                   factor, the highest kept                  (R >= 4)
+ *   W4_ROPE_YARN    f_i (1 - g_i) + f_i / factor * g_i; pairs that turn 32 times or more over the
+ *                   original `context` positions keep f_i (g = 0), pairs that turn once or less
+ *                   are divided (g = 1), linear in i between those two dimensions; the amplitude
+ *                   is 0.1 ln(factor) + 1.  ("YaRN: Efficient Context Window Extension of Large
+ *                   Language Models", arXiv 2309.00071, sections 3.2 - 3.4)
+ * Computed in 64 bits and rounded once.
+ *   inv_freq   HOST fp32 [R / 2], out;   amplitude  HOST fp32, out, may be NULL (1 but for YARN)
+ * Errors: W4_ERR_NULL, W4_ERR_SHAPE (rot_dim), W4_ERR_RANGE (base <= 1, factor < 1, context < 1 or
+ * any of them not finite), W4_ERR_UNSUPPORTED (an unknown scaling).
+ */
+int w4_rope_frequencies(int rot_dim, int scaling, double base, double factor, double context,
+                        float *inv_freq, float *amplitude);
+
+/*
+ * w4_rope_append -- rotary positions on the fused q/k/v projection of T tokens, the rotated keys
+ * and the values appended to the cache.  Per token at position p, per q and k head, for the first
+ * rot_dim dimensions in pairs (a, b):
+ *   t = p * inv_freq[i];   a' = factor (a cos t - b sin t),   b' = factor (a sin t + b cos t)
+ * the other dimensions of q and k, and v, are copied bit for bit.  The angle keeps full precision
+ * at any position: it is reduced modulo one turn in 64 bits.
+ *   qkv       bf16 [T][ldqkv], the n_heads query heads, then the key heads, then the value heads,
+ *             each of head_dim; ldqkv % 8 == 0, 16-byte aligned (the output of a w4 linear)
+ *   q_start   int32 [n_seqs + 1], or NULL: one token per sequence (T = n_seqs)
+ *   inv_freq  fp32 [rot_dim / 2], rot_dim even, 2 .. head_dim;  factor  finite
+ *   q         bf16 [T][ldq], ldq >= n_heads * head_dim, ldq % 8 == 0, 16-byte aligned
+ * Tokens at negative positions, or whose page table entry lies outside the cache, are not
+ * appended; their q row is written all the same.
+ */
+int w4_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int n_heads,
+                   const int32_t *q_start, const float *inv_freq, int rot_dim, int layout,
+                   float factor, const w4_kv_cache *cache, uint16_t *q, int64_t ldq,
+                   void *stream);
+
+/*
+ * w4_attn_decode -- attention of one new token per sequence over the cache, the token at position
+ * kv_len[b] - 1:
+ *   s_j = scale * q . k_j,   y = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = ln sum_j exp(s_j)
+ * over the visible keys j; query head h reads key-value head h / (n_heads / n_kv_heads).  A token
+ * that sees no key gets y = 0 and lse = -inf.
+ *   q      bf16 [n_seqs][ldq], head h at element h * head_dim; ldq % 8 == 0, 16-byte aligned
+ *   scale  finite, >= 0
+ *   y      [n_seqs][ldy], ldy >= n_heads * head_dim, element type out_dtype, naturally aligned
+ *   lse    fp32 [n_seqs][n_heads] or NULL
+ *   work   device memory of at least w4_attn_decode_work_bytes bytes, 16-byte aligned, as for
+ *          w4_gemv_ws; may be NULL when that size is 0
+ * Long caches are split over several compute units and joined in order (deterministic).
+ * w4_attn_decode_work_bytes reads only sizes, no array; 0 for arguments the call rejects.
+ */
+int w4_attn_decode(const uint16_t *q, int64_t ldq, int n_heads, const w4_kv_cache *cache,
+                   float scale, int64_t window, int64_t sinks, void *y, int64_t ldy,
+                   int out_dtype, float *lse, void *work, size_t work_bytes, void *stream);
+size_t w4_attn_decode_work_bytes(int n_heads, const w4_kv_cache *cache, int64_t window,
+                                 int64_t sinks);
+
+/*
+ * w4_attn_prefill -- the same attention for T tokens of n_seqs sequences (token rows as above),
+ * each at its own position: prompts, chunks of prompts, or several new tokens per sequence.
+ *   q      bf16 [T][ldq];  q_start int32 [n_seqs + 1];  y [T][ldy];  lse fp32 [T][n_heads] or NULL
+ *   the other arguments as for w4_attn_decode.
+ * The softmax weights enter the second product as bf16, their sum in fp32.
+ */
+int w4_attn_prefill(const uint16_t *q, int64_t T, int64_t ldq, int n_heads,
+                    const int32_t *q_start, const w4_kv_cache *cache, float scale,
+                    int64_t window, int64_t sinks, void *y, int64_t ldy, int out_dtype,
+                    float *lse, void *work, size_t work_bytes, void *stream);
+size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache,
+                                  int64_t window, int64_t sinks);
+
+/*
+ * w4_residual_norm -- the seam between two blocks of a layer: the norm after a block, its gate and
+ * residual scale, the residual add, and the norm before the next block, in one pass:
+ *   n = x,  or  rms(x, w_post) where w_post is given
+ *   r' = r + alpha * g * n         (g = 1 without a gate)
+ *   y = rms(r', w_pre),            rms(u, w) = u / sqrt(mean(u^2) + eps) * (w + weight_offset)
+ * All in fp32; r' is rounded once to its own type, y once to bf16 (from the unrounded r').
+ *   x         bf16 [T][ldx], or NULL: y = rms(r, w_pre) alone (w_post, gate, r_out then NULL too)
+ *   r         [T][ldr], r_dtype W4_OUT_BF16 or W4_OUT_F32
+ *   w_post    bf16 [d] or NULL;  w_pre bf16 [d]
+ *   gate      bf16 [T][ldg], or one vector [d] for all tokens with ldg = 0, or NULL
+ *   alpha, weight_offset  finite;  eps  finite, >= 0
+ *   r_out     as r, [T][ldr_out]; may be r itself (with ldr_out = ldr), else no overlap
+ *   y         bf16 [T][ldy]
+ * d <= W4_NORM_MAX_D (W4_ERR_RANGE beyond).  Leading dimensions are >= d and otherwise free;
+ * pointers are naturally aligned.  (Rows that start at 16-byte boundaries are read faster.)
+ */
+int w4_residual_norm(const uint16_t *x, int64_t ldx, const void *r, int64_t ldr, int r_dtype,
+                     int64_t T, int64_t d, const uint16_t *w_post, const uint16_t *w_pre,
+                     float weight_offset, const uint16_t *gate, int64_t ldg, float alpha,
+                     float eps, void *r_out, int64_t ldr_out, uint16_t *y, int64_t ldy,
+                     void *stream);
 
 /* Text for a w4_status value (static storage). */
 const char *w4_status_string(int status);

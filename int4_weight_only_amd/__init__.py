@@ -20,15 +20,32 @@ __all__ = [
     "w4_qat_repack", "gptq_hessian", "gptq_factor", "gptq_quantize", "gptq_quantize_noalloc",
     "gptq",
     "w4_linear",
+    "W4_ROPE_HALF", "W4_ROPE_INTERLEAVED", "W4_ROPE_PLAIN", "W4_ROPE_LINEAR", "W4_ROPE_NTK",
+    "W4_ROPE_YARN", "w4_rope_frequencies", "w4_rope_append", "w4_attn_decode",
+    "w4_attn_decode_work_bytes", "w4_attn_prefill", "w4_attn_prefill_work_bytes",
+    "w4_residual_norm",
     "library_path",
 ]
 
 W4_SYM, W4_ASYM = 0, 1
 W4_OUT_BF16, W4_OUT_F32 = 0, 1
+W4_ROPE_HALF, W4_ROPE_INTERLEAVED = 0, 1
+W4_ROPE_PLAIN, W4_ROPE_LINEAR, W4_ROPE_NTK, W4_ROPE_YARN = 0, 1, 2, 3
 GEMV_MAX_M = 64
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libw4.so")
+
+
+class _KvCache(ctypes.Structure):
+    """w4_kv_cache of include/w4.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("n_pages", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("slot_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_table", ctypes.c_void_p), ("n_seqs", ctypes.c_int64),
+                ("table_cols", ctypes.c_int64), ("ld_table", ctypes.c_int64),
+                ("kv_len", ctypes.c_void_p)]
 
 
 class W4Error(RuntimeError):
@@ -63,6 +80,21 @@ def _load(path):
     lib.w4a8_gemv.argtypes = [p, p, i64, i64, p, p, p, i64, i64, p, i64, i32, p, p]
     lib.w4a8_gemm.argtypes = lib.w4a8_gemv.argtypes
     lib.w4a8_linear.argtypes = [p, i64, i64, p, p, p, i64, i64, p, i64, i32, p, p, p]
+    cache, f32, f64 = ctypes.POINTER(_KvCache), ctypes.c_float, ctypes.c_double
+    lib.w4_rope_frequencies.argtypes = [i32, i32, f64, f64, f64, p, p]
+    lib.w4_rope_append.argtypes = [p, i64, i64, i32, p, p, i32, i32, f32, cache, p, i64, p]
+    attn = [f32, i64, i64, p, i64, i32, p, p, ctypes.c_size_t, p]
+    lib.w4_attn_decode.argtypes = [p, i64, i32, cache] + attn
+    lib.w4_attn_decode_work_bytes.argtypes = [i32, cache, i64, i64]
+    lib.w4_attn_decode_work_bytes.restype = ctypes.c_size_t
+    lib.w4_attn_prefill.argtypes = [p, i64, i64, i32, p, cache] + attn
+    lib.w4_attn_prefill_work_bytes.argtypes = [i64, i32, cache, i64, i64]
+    lib.w4_attn_prefill_work_bytes.restype = ctypes.c_size_t
+    lib.w4_residual_norm.argtypes = [p, i64, p, i64, i32, i64, i64, p, p, f32, p, i64, f32, f32,
+                                     p, i64, p, i64, p]
+    for f in ("w4_rope_frequencies", "w4_rope_append", "w4_attn_decode", "w4_attn_prefill",
+              "w4_residual_norm"):
+        getattr(lib, f).restype = i32
     for f in ("w4_packed_layout", "w4_pack", "w4_qat_repack", "w4_gptq_hessian", "w4_gptq_factor",
               "w4_gptq_quantize", "w4_gptq_quantize_noalloc", "w4_gemv", "w4_gemv_ws",
               "w4_gemv_glu", "w4_gemm",
@@ -474,3 +506,171 @@ def w4a8_linear(x, qweight, s_w, bias, d_in, out_dtype=W4_OUT_BF16, want_acc=Fal
                                            out_dtype, _ptr(s_x), _ptr(acc), _stream(dev)))
     res = (out,) + ((acc,) if want_acc else ()) + ((s_x,) if want_scales else ())
     return res if len(res) > 1 else out
+
+
+def w4_rope_frequencies(rot_dim, scaling=W4_ROPE_PLAIN, base=10000.0, factor=1.0, context=1.0):
+    """(inv_freq fp32 [rot_dim / 2], amplitude) of rotary positions for a context scaling (host
+    only; move inv_freq to the GPU once)."""
+    inv_freq = torch.empty(max(rot_dim, 2) // 2, dtype=torch.float32)
+    amplitude = ctypes.c_float()
+    _check("w4_rope_frequencies", _lib.w4_rope_frequencies(
+        rot_dim, scaling, base, factor, context, _ptr(inv_freq), ctypes.byref(amplitude)))
+    return inv_freq, amplitude.value
+
+
+def _kv_cache(k_cache, v_cache, page_table, kv_len, dev):
+    """The ABI's view of a cache [n_pages][page_size][n_kv_heads][head_dim] (any strides with the
+    last dim contiguous; another order of slots and heads is a permuted view)."""
+    _need(k_cache, "k_cache", torch.bfloat16, dev, 4)
+    _need(v_cache, "v_cache", torch.bfloat16, dev, 4)
+    _need(page_table, "page_table", torch.int32, dev, 2)
+    _need(kv_len, "kv_len", torch.int32, dev, 1)
+    n_pages, page_size, n_kv, D = k_cache.shape
+    # the stride of a dimension of one element says nothing
+    sp, ss, sh, _ = (s if n > 1 else 0 for n, s in zip(k_cache.shape, k_cache.stride()))
+    if v_cache.shape != k_cache.shape or any(
+            n > 1 and s != t for n, s, t in zip(k_cache.shape, k_cache.stride(), v_cache.stride())):
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    n_seqs, cols = page_table.shape
+    if kv_len.shape[0] != n_seqs:
+        raise ValueError(f"kv_len must have {n_seqs} elements")
+    return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), n_pages, sp, ss, sh, page_size, n_kv,
+                    D, page_table.data_ptr(), n_seqs, cols,
+                    page_table.stride(0) if n_seqs > 1 else cols, kv_len.data_ptr())
+
+
+def _need_q_start(q_start, n_seqs, dev):
+    _need(q_start, "q_start", torch.int32, dev, 1)
+    if q_start.shape[0] != n_seqs + 1:
+        raise ValueError(f"q_start must have {n_seqs + 1} elements")
+
+
+def w4_rope_append(qkv, n_heads, k_cache, v_cache, page_table, kv_len, inv_freq, q_start=None,
+                   layout=W4_ROPE_HALF, factor=1.0, out=None):
+    """Rotary positions on the fused projection qkv bf16 [T][(n_heads + 2 n_kv) head_dim]; the
+    rotated keys and the values are written to the cache, the rotated queries returned
+    ([T][n_heads * head_dim]).  kv_len counts the T tokens already; q_start int32 [n_seqs + 1] gives
+    each sequence's rows (None: one token per sequence)."""
+    _need(qkv, "qkv", torch.bfloat16, dim=2)
+    dev = qkv.device
+    _need(inv_freq, "inv_freq", torch.float32, dev, 1)
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, dev)
+    if q_start is not None:
+        _need_q_start(q_start, cache.n_seqs, dev)
+    T, width = qkv.shape
+    if width < (n_heads + 2 * cache.n_kv_heads) * cache.head_dim:
+        raise ValueError(f"qkv has {width} columns, fewer than its heads")
+    out = _out(out, T, n_heads * cache.head_dim, torch.bfloat16, dev)
+    _check("w4_rope_append", _lib.w4_rope_append(
+        _ptr(qkv), T, qkv.stride(0) if T > 1 else width, n_heads, _ptr(q_start), _ptr(inv_freq),
+        2 * inv_freq.shape[0], layout, factor, ctypes.byref(cache), _ptr(out),
+        out.stride(0) if T > 1 else out.shape[1], _stream(dev)))
+    return out
+
+
+def _attention(name, q, k_cache, v_cache, page_table, kv_len, q_start, scale, window, sinks,
+               out_dtype, out, want_lse, work):
+    _need(q, "q", torch.bfloat16, dim=2)
+    dev = q.device
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, dev)
+    T, width = q.shape
+    D = cache.head_dim
+    if width % D != 0:
+        raise ValueError(f"q has {width} columns, not a multiple of head_dim={D}")
+    n_heads = width // D
+    lead = [_ptr(q), q.stride(0) if T > 1 else width, n_heads]
+    if q_start is None:
+        if T != cache.n_seqs:
+            raise ValueError(f"q must have one row for each of {cache.n_seqs} sequences")
+        need = _lib.w4_attn_decode_work_bytes(n_heads, ctypes.byref(cache), window, sinks)
+    else:
+        _need_q_start(q_start, cache.n_seqs, dev)
+        lead = [lead[0], T, lead[1], n_heads, _ptr(q_start)]
+        need = _lib.w4_attn_prefill_work_bytes(T, n_heads, ctypes.byref(cache), window, sinks)
+    if work is None:
+        if need:
+            work = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(work, "work", torch.uint8, dev, 1)
+    tdtype = torch.float32 if out_dtype == W4_OUT_F32 else torch.bfloat16
+    out = _out(out, T, width, tdtype, dev)
+    lse = torch.empty((T, n_heads), dtype=torch.float32, device=dev) if want_lse else None
+    _check(name, getattr(_lib, name)(
+        *lead, ctypes.byref(cache), D ** -0.5 if scale is None else scale, window, sinks,
+        _ptr(out), out.stride(0) if T > 1 else width, out_dtype, _ptr(lse), _ptr(work),
+        0 if work is None else work.numel(), _stream(dev)))
+    return (out, lse) if want_lse else out
+
+
+def w4_attn_decode(q, k_cache, v_cache, page_table, kv_len, scale=None, window=0, sinks=0,
+                   out_dtype=W4_OUT_BF16, out=None, want_lse=False, work=None):
+    """Attention of one new token per sequence (q bf16 [n_seqs][n_heads * head_dim], at position
+    kv_len - 1) over the paged cache; scale None: 1 / sqrt(head_dim).  Returns y [n_seqs][width],
+    or (y, lse fp32 [n_seqs][n_heads]) when want_lse.  work: a uint8 tensor of at least
+    w4_attn_decode_work_bytes bytes (None: one is allocated where needed)."""
+    return _attention("w4_attn_decode", q, k_cache, v_cache, page_table, kv_len, None, scale,
+                      window, sinks, out_dtype, out, want_lse, work)
+
+
+def w4_attn_prefill(q, k_cache, v_cache, page_table, kv_len, q_start, scale=None, window=0,
+                    sinks=0, out_dtype=W4_OUT_BF16, out=None, want_lse=False, work=None):
+    """w4_attn_decode for T tokens of n_seqs sequences, the rows q_start[b] .. q_start[b + 1] - 1 of
+    q being the last tokens of sequence b: prompts, chunks, or several new tokens each."""
+    if q_start is None:
+        raise TypeError("q_start must be a torch.Tensor")
+    return _attention("w4_attn_prefill", q, k_cache, v_cache, page_table, kv_len, q_start, scale,
+                      window, sinks, out_dtype, out, want_lse, work)
+
+
+def w4_attn_decode_work_bytes(n_heads, k_cache, v_cache, page_table, kv_len, window=0, sinks=0):
+    """Bytes of workspace w4_attn_decode needs for these sizes (0: none)."""
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, k_cache.device)
+    return int(_lib.w4_attn_decode_work_bytes(n_heads, ctypes.byref(cache), window, sinks))
+
+
+def w4_attn_prefill_work_bytes(T, n_heads, k_cache, v_cache, page_table, kv_len, window=0,
+                               sinks=0):
+    """Bytes of workspace w4_attn_prefill needs for these sizes (0: none)."""
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, k_cache.device)
+    return int(_lib.w4_attn_prefill_work_bytes(T, n_heads, ctypes.byref(cache), window, sinks))
+
+
+def w4_residual_norm(x, residual, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6,
+                     weight_offset=0.0, out=None, residual_out=None):
+    """The seam between two blocks: residual_out = residual + alpha * gate * n with n = x or
+    rms(x, w_post), and y = rms(residual_out, w_pre).  x bf16 [T][d] (None: y = rms(residual,
+    w_pre) alone), residual bf16 or fp32 [T][d], gate bf16 [d] or [T][d].  residual_out may be
+    `residual` itself.  Returns (y bf16 [T][d], residual_out)."""
+    if not isinstance(residual, torch.Tensor) or residual.dtype not in (torch.bfloat16,
+                                                                         torch.float32):
+        raise TypeError("residual must be a torch.bfloat16 or torch.float32 tensor")
+    _need(residual, "residual", residual.dtype, dim=2)
+    dev = residual.device
+    T, d = residual.shape
+    _need(w_pre, "w_pre", torch.bfloat16, dev, 1)
+    if w_post is not None:
+        _need(w_post, "w_post", torch.bfloat16, dev, 1)
+    if w_pre.shape[0] != d or (w_post is not None and w_post.shape[0] != d):
+        raise ValueError(f"w_pre and w_post must have {d} elements")
+    ldx = ldg = ldro = 0
+    if x is not None:
+        _need(x, "x", torch.bfloat16, dev, 2)
+        if tuple(x.shape) != (T, d):
+            raise ValueError(f"x must be [{T}][{d}]")
+        ldx = x.stride(0) if T > 1 else d
+        residual_out = _out(residual_out, T, d, residual.dtype, dev)
+        ldro = residual_out.stride(0) if T > 1 else d
+    elif residual_out is not None:
+        raise ValueError("residual_out needs x")
+    if gate is not None:
+        _need(gate, "gate", torch.bfloat16, dev)
+        if tuple(gate.shape) not in ((d,), (T, d)):
+            raise ValueError(f"gate must be [{d}] or [{T}][{d}]")
+        ldg = gate.stride(0) if gate.dim() == 2 and T > 1 else 0
+    y = _out(out, T, d, torch.bfloat16, dev)
+    _check("w4_residual_norm", _lib.w4_residual_norm(
+        _ptr(x), ldx, _ptr(residual), residual.stride(0) if T > 1 else d,
+        W4_OUT_F32 if residual.dtype == torch.float32 else W4_OUT_BF16, T, d, _ptr(w_post),
+        _ptr(w_pre), weight_offset, _ptr(gate), ldg, alpha, eps, _ptr(residual_out), ldro,
+        _ptr(y), y.stride(0) if T > 1 else d, _stream(dev)))
+    return y, (residual if x is None else residual_out)

@@ -14,10 +14,7 @@ namespace {
 
 thread_local std::string g_last_hip_error;
 
-int hip_fail(hipError_t err) {
-    g_last_hip_error = hipGetErrorString(err);
-    return W4_ERR_HIP;
-}
+using w4::hip_fail;
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -366,6 +363,11 @@ int w4a8_linear(const uint16_t *x, int64_t M, int64_t ldx, const uint8_t *qweigh
 }  // extern "C"
 
 namespace w4 {
+
+int hip_fail(hipError_t err) {
+    g_last_hip_error = hipGetErrorString(err);
+    return W4_ERR_HIP;
+}
 
 int device_cu_count() {
     static std::mutex mu;

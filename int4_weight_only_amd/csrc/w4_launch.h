@@ -3,7 +3,10 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stddef.h>
 #include <stdint.h>
+
+#include "kv_device.h"
 
 namespace w4 {
 
@@ -129,6 +132,49 @@ hipError_t launch_gemv_i8(const uint16_t *x, int64_t M, int64_t ldx, const uint8
                           int64_t d_out, int64_t d_in, int64_t k_pad, int64_t span,
                           int64_t n_groups, void *y, int64_t ldy, bool out_f32, bool glu,
                           hipStream_t stream);
+
+// Rotary positions with the cache append (rope.hip).
+hipError_t launch_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int n_heads,
+                              const int32_t *q_start, const float *inv_freq, int rot_dim,
+                              bool interleaved, float factor, const KvView &cache, uint16_t *q,
+                              int64_t ldq, hipStream_t stream);
+
+// Attention over the paged cache (attn_decode.hip, attn_prefill.hip).
+struct AttnArgs {
+    const uint16_t *q;
+    int64_t T, ldq;
+    int n_heads;
+    const int32_t *q_start;  // NULL: one row per sequence
+    float scale;
+    int window, sinks;  // window 0: none
+    void *y;
+    int64_t ldy;
+    bool out_f32;
+    float *lse;
+    void *work;
+};
+size_t attn_decode_work_bytes(int n_heads, const KvView &cache, int window, int sinks);
+hipError_t launch_attn_decode(const AttnArgs &a, const KvView &cache, hipStream_t stream);
+size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &cache, int window, int sinks);
+hipError_t launch_attn_prefill(const AttnArgs &a, const KvView &cache, hipStream_t stream);
+
+// The residual norm (norm.hip); pointers checked, r and r_out of the type r_f32 says.
+struct NormArgs {
+    const uint16_t *x;
+    const void *r;
+    const uint16_t *w_post, *w_pre, *gate;
+    void *r_out;
+    uint16_t *y;
+    int64_t ldx, ldr, ldg, ldr_out, ldy;
+    int64_t T;
+    int d;
+    bool r_f32;
+    float weight_offset, alpha, eps;
+};
+hipError_t launch_residual_norm(const NormArgs &a, hipStream_t stream);
+
+// Records the text of a failed HIP call for w4_last_hip_error; returns W4_ERR_HIP.
+int hip_fail(hipError_t err);
 
 // Number of compute units of the current device (cached per device).
 int device_cu_count();
