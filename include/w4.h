@@ -438,7 +438,8 @@ size_t w4_attn_decode_work_bytes(int n_heads, const w4_kv_cache *cache, int64_t 
  * each at its own position: prompts, chunks of prompts, or several new tokens per sequence.
  *   q      bf16 [T][ldq];  q_start int32 [n_seqs + 1];  y [T][ldy];  lse fp32 [T][n_heads] or NULL
  *   the other arguments as for w4_attn_decode.
- * The softmax weights enter the second product as bf16, their sum in fp32.
+ * T * n_heads and n_seqs * n_heads must be below 2^31 (W4_ERR_RANGE; n_seqs * n_heads also for
+ * w4_attn_decode).  The softmax weights enter the second product as bf16, their sum in fp32.
  */
 int w4_attn_prefill(const uint16_t *q, int64_t T, int64_t ldq, int n_heads,
                     const int32_t *q_start, const w4_kv_cache *cache, float scale,

@@ -88,6 +88,9 @@ int check_attn(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int
     const int64_t width = static_cast<int64_t>(n_heads) * view->head_dim;
     if (T < 1 || ldq < width || ldy < width) return W4_ERR_SHAPE;
     if (T > W4_MAX_DIM || ldq > W4_MAX_DIM || ldy > W4_MAX_DIM) return W4_ERR_RANGE;
+    // the kernels count (token, head) pairs and workgroups in 31 bits
+    if (T * n_heads > INT32_MAX || view->n_seqs * static_cast<int64_t>(n_heads) > INT32_MAX)
+        return W4_ERR_RANGE;
     if (out_dtype != W4_OUT_BF16 && out_dtype != W4_OUT_F32) return W4_ERR_UNSUPPORTED;
     if (!std::isfinite(scale) || scale < 0.0f) return W4_ERR_RANGE;
     if (int st = check_mask(window, sinks, *view, a)) return st;

@@ -1,0 +1,61 @@
+// attn_device.h -- pieces shared by the attention kernels: matrix-core types, the layout of key
+// and value tiles in LDS, the join of partial results.
+#pragma once
+
+#include "w4_device.h"
+#include "w4_launch.h"
+
+namespace w4 {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef short short4_t __attribute__((ext_vector_type(4)));
+typedef float floatx4_t __attribute__((ext_vector_type(4)));
+typedef float floatx16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t uintx2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t uintx4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNoMax = -1e30f;  // running maximum before the first key (finite: no inf - inf)
+
+// Two fp32 values as bf16 (round to nearest even) in one dword, the first in the low half.
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    bf16x2_t r;
+    r[0] = static_cast<__bf16>(a);
+    r[1] = static_cast<__bf16>(b);
+    return __builtin_bit_cast(uint32_t, r);
+}
+
+// Four bf16 rows of 16 columns, transposed on the way out of LDS: in each group of 16 lanes, lane i
+// addresses the 8 bytes at columns 4 (i % 4) of row i / 4 and receives column i of the four rows.
+__device__ __forceinline__ uintx2_t lds_read_transposed(const uint16_t *p) {
+    typedef __attribute__((address_space(3))) short4_t *lds_t;
+    return __builtin_bit_cast(uintx2_t,
+                              __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p)));
+}
+
+// Index (in 16-byte chunks) of chunk c of row r in a tile of rows of DP bf16, swizzled against bank
+// conflicts (64 banks of 4 bytes, 16 chunks wide).
+//   keys:   a fragment reads one chunk of 16 or 32 consecutive rows, a store one row: the chunk
+//           number is xor-ed with the row's, counted in rows of 256 bytes.
+//   values: a transposed read takes a pair of chunks of 4 consecutive rows at once: xor-ed with
+//           twice the row, which keeps the pair together.
+template <int DP>
+__device__ __forceinline__ int key_slot(int r, int c) {
+    constexpr int kChunks = DP / 8;
+    if constexpr (kChunks >= 16) return r * kChunks + (c ^ (r & 15));
+    else return r * kChunks + (c ^ ((r >> 1) & (kChunks - 1)));
+}
+template <int DP>
+__device__ __forceinline__ int value_slot(int r, int c) {
+    constexpr int kChunks = DP / 8;
+    if constexpr (kChunks >= 16) return r * kChunks + (c ^ (2 * (r & 7)));
+    else return r * kChunks + (c ^ (2 * (r & 3)));
+}
+
+__device__ __forceinline__ float other_half(float v) {  // the value of lane ^ 32
+    return __shfl_xor(v, 32, kWave);
+}
+
+}  // namespace w4
