@@ -337,7 +337,8 @@ int w4a8_gemm(const int8_t *q, const float *s_x, int64_t M, int64_t ldq, const u
  *               elements spanned inside one page must be fewer than 2^31
  *   page_size   slots of a page, a power of two, 1 .. 32768
  *   n_kv_heads  1 .. 1024;   head_dim  a multiple of 8, 8 .. 256
- *   page_table  int32 [n_seqs][ld_table], table_cols entries used: position p of sequence b lives
+ *   page_table  int32 [n_seqs][ld_table], table_cols entries used (table_cols * page_size up to
+ *               2^30 positions): position p of sequence b lives
  *               in slot p % page_size of page page_table[b][p / page_size].  Only entries of
  *               positions that an operator reads or writes matter; the others may hold anything.
  *               An entry outside [0, n_pages) never makes an access leave the cache (reads see

@@ -31,7 +31,7 @@ int check_cache(const w4_kv_cache *c, int n_heads, w4::KvView *view) {
         return W4_ERR_SHAPE;
     if (c->n_pages > INT32_MAX || c->n_kv_heads > W4_MAX_HEADS || n_heads > W4_MAX_HEADS ||
         c->head_dim > W4_MAX_HEAD_DIM || c->page_size > 32768 || c->n_seqs > W4_MAX_DIM ||
-        c->ld_table > INT32_MAX || c->table_cols > INT32_MAX / c->page_size)
+        c->ld_table > INT32_MAX || c->table_cols > (1 << 30) / c->page_size)
         return W4_ERR_RANGE;
     if (n_heads % c->n_kv_heads != 0) return W4_ERR_SHAPE;
     if (c->head_dim % 8 != 0 || (c->page_size & (c->page_size - 1)) != 0)

@@ -54,6 +54,24 @@ __device__ __forceinline__ int value_slot(int r, int c) {
     else return r * kChunks + (c ^ (2 * (r & 3)));
 }
 
+// Four consecutive elements of an output row, from element idx (a multiple of 4) on. `wide`: the
+// output's base and rows allow one store.
+__device__ __forceinline__ void store_out4(void *y, int64_t idx, floatx4_t v, bool out_f32,
+                                           bool wide) {
+    if (!wide) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_out(y, idx + i, v[i], out_f32);
+    } else if (out_f32) {
+        *reinterpret_cast<floatx4_t *>(static_cast<float *>(y) + idx) = v;
+    } else {
+        const uintx2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+        *reinterpret_cast<uintx2_t *>(static_cast<uint16_t *>(y) + idx) = w;
+    }
+}
+__device__ __forceinline__ bool wide_rows(const AttnArgs &a) {
+    return (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+}
+
 __device__ __forceinline__ float other_half(float v) {  // the value of lane ^ 32
     return __shfl_xor(v, 32, kWave);
 }

@@ -274,7 +274,7 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     if (a.lse && half == 0)
         a.lse[token * a.n_heads + head] = l > 0.0f ? M * kLn2 + logf(l) : -INFINITY;
     const int64_t base = token * a.ldy + static_cast<int64_t>(head) * D;
-    const bool wide = (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
+    const bool wide = wide_rows(a);
 #pragma unroll
     for (int d = 0; d < DT; ++d)
 #pragma unroll
@@ -284,15 +284,7 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
             floatx4_t v;
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = o[d][4 * g + i] * inv;
-            if (!wide) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) store_out(a.y, base + col + i, v[i], a.out_f32);
-            } else if (a.out_f32) {
-                *reinterpret_cast<floatx4_t *>(static_cast<float *>(a.y) + base + col) = v;
-            } else {
-                const uintx2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-                *reinterpret_cast<uintx2_t *>(static_cast<uint16_t *>(a.y) + base + col) = w;
-            }
+            store_out4(a.y, base + col, v, a.out_f32, wide);
         }
 }
 
