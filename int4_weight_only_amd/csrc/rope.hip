@@ -20,54 +20,140 @@ __device__ __forceinline__ void turn(int pos, float inv_freq, float factor, floa
     *s = factor * sinpif(2.0f * t);
 }
 
-// One wave per (token, head).
-__global__ void __launch_bounds__(64) rope_append_kernel(
+// One workgroup per token. The angles of its R / 2 pairs are computed once, into LDS, and serve
+// every query and key head; the heads' values move in 16-byte pieces: `u` rotated pieces of a head
+// (LAYOUT half: 8 pairs, read and written as two pieces R / 2 apart; interleaved: 4 pairs, one
+// piece), then the pieces past R and the value heads, copied. ANY: heads whose R does not fall on
+// those pieces (R % 16 for the half layout, R % 8 for the interleaved), element by element.
+enum { kHalf = 0, kInterleaved = 1, kAny = 2 };
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = 128;
+
+typedef uint32_t uintx4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ void unpack8(const uint16_t *p, float *v) {
+    const uintx4_t w = *reinterpret_cast<const uintx4_t *>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+__device__ __forceinline__ void pack8(uint16_t *p, const float *v) {
+    uintx4_t w;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
+    *reinterpret_cast<uintx4_t *>(p) = w;
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(kThreads) rope_append_kernel(
     const uint16_t *__restrict__ qkv, int64_t ldqkv, int n_heads,
     const int32_t *__restrict__ q_start, const float *__restrict__ inv_freq, int rot_dim,
-    int interleaved, float factor, KvView c, uint16_t *__restrict__ q, int64_t ldq) {
-    const int t = blockIdx.x, h = blockIdx.y, lane = threadIdx.x;
-    const int D = c.head_dim;
-    const uint16_t *src = qkv + t * ldqkv + static_cast<int64_t>(h) * D;
+    int interleaved, float factor, KvView c, uint16_t *__restrict__ q, int64_t ldq,
+    int width_shift) {
+    __shared__ float cosine[kMaxPairs], sine[kMaxPairs];
+    const int64_t t = blockIdx.x;
+    const int tid = threadIdx.x, D = c.head_dim, half = rot_dim / 2;
     RowPlace at;
-    if (!place_of_row(c, q_start, t, &at)) return;
-    const int pos = at.pos;
-    uint16_t *dst;
-    if (h < n_heads) {
-        dst = q + t * ldq + static_cast<int64_t>(h) * D;
-    } else {
-        if (pos < 0) return;
-        const int32_t *row = c.table + at.seq * c.ld_table;
-        const int page = row[pos >> c.page_shift];
-        if (page < 0 || page >= c.n_pages) return;
-        const int hk = h - n_heads;
-        dst = (hk < c.n_kv ? c.k : c.v) + kv_offset(c, row, pos, hk < c.n_kv ? hk : hk - c.n_kv);
+    if (!place_of_row(c, q_start, static_cast<int>(t), &at)) return;
+    for (int i = tid; i < half; i += blockDim.x)
+        turn(at.pos, inv_freq[i], factor, &cosine[i], &sine[i]);
+    // the token's slot in the cache, if it is appended
+    int64_t slot = -1;
+    if (at.pos >= 0) {
+        const int page = c.table[at.seq * c.ld_table + (at.pos >> c.page_shift)];
+        if (page >= 0 && page < c.n_pages)
+            slot = static_cast<int64_t>(page) * c.page_stride +
+                   static_cast<int64_t>((at.pos & c.page_mask) * c.slot_stride);
     }
-    const int half = rot_dim / 2;
-    if (h < n_heads + c.n_kv) {
-        for (int i = lane; i < half; i += 64) {
-            const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + half;
-            const float xa = bf16_to_f32(src[ia]), xb = bf16_to_f32(src[ib]);
-            float cs, sn;
-            turn(pos, inv_freq[i], factor, &cs, &sn);
-            dst[ia] = f32_to_bf16(xa * cs - xb * sn);
-            dst[ib] = f32_to_bf16(xa * sn + xb * cs);
+    __syncthreads();
+    // threads over (head, piece): 2^width_shift of them a head
+    const int piece0 = tid & ((1 << width_shift) - 1);
+    const int n_rotate = n_heads + c.n_kv;
+    for (int h = tid >> width_shift; h < n_rotate + c.n_kv; h += blockDim.x >> width_shift) {
+        const uint16_t *src = qkv + t * ldqkv + static_cast<int64_t>(h) * D;
+        uint16_t *dst = q + t * ldq + static_cast<int64_t>(h) * D;
+        if (h >= n_heads) {
+            if (slot < 0) break;
+            const int hk = h - n_heads;
+            dst = hk < c.n_kv ? c.k + slot + static_cast<int64_t>(hk) * c.head_stride
+                              : c.v + slot + static_cast<int64_t>(hk - c.n_kv) * c.head_stride;
         }
-        for (int i = rot_dim + lane; i < D; i += 64) dst[i] = src[i];
-    } else {
-        for (int i = lane; i < D; i += 64) dst[i] = src[i];
+        const int rotated = h < n_rotate ? (MODE == kHalf ? half / 8 : rot_dim / 8) : 0;
+        const int pieces = h < n_rotate ? rotated + (D - rot_dim) / 8 : D / 8;
+        if (MODE == kAny && h < n_rotate) {
+            for (int i = piece0; i < half; i += 1 << width_shift) {
+                const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + half;
+                const float xa = bf16_to_f32(src[ia]), xb = bf16_to_f32(src[ib]);
+                dst[ia] = static_cast<uint16_t>(f32_to_bf16(xa * cosine[i] - xb * sine[i]));
+                dst[ib] = static_cast<uint16_t>(f32_to_bf16(xa * sine[i] + xb * cosine[i]));
+            }
+            for (int i = rot_dim + piece0; i < D; i += 1 << width_shift) dst[i] = src[i];
+            continue;
+        }
+        for (int p = piece0; p < pieces; p += 1 << width_shift) {
+            if (p >= rotated) {
+                const int d = (h < n_rotate ? rot_dim : 0) + 8 * (p - rotated);
+                *reinterpret_cast<uintx4_t *>(dst + d) =
+                    *reinterpret_cast<const uintx4_t *>(src + d);
+            } else if (MODE == kHalf) {
+                float a[8], b[8], x[8], y[8];
+                unpack8(src + 8 * p, a);
+                unpack8(src + 8 * p + half, b);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float cs = cosine[8 * p + i], sn = sine[8 * p + i];
+                    x[i] = a[i] * cs - b[i] * sn;
+                    y[i] = a[i] * sn + b[i] * cs;
+                }
+                pack8(dst + 8 * p, x);
+                pack8(dst + 8 * p + half, y);
+            } else {
+                float a[8], x[8];
+                unpack8(src + 8 * p, a);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float cs = cosine[4 * p + i], sn = sine[4 * p + i];
+                    x[2 * i] = a[2 * i] * cs - a[2 * i + 1] * sn;
+                    x[2 * i + 1] = a[2 * i] * sn + a[2 * i + 1] * cs;
+                }
+                pack8(dst + 8 * p, x);
+            }
+        }
     }
+}
+
+template <int MODE, typename... Args>
+hipError_t launch(int64_t T, int threads, hipStream_t stream, Args... args) {
+    hipLaunchKernelGGL(rope_append_kernel<MODE>, dim3(static_cast<unsigned>(T)), dim3(threads), 0,
+                       stream, args...);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int n_heads,
                               const int32_t *q_start, const float *inv_freq, int rot_dim,
-                              bool interleaved, float factor, const KvView &cache, uint16_t *q,
+                              bool interleaved, float factor, const KvView &c, uint16_t *q,
                               int64_t ldq, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(n_heads + 2 * cache.n_kv));
-    hipLaunchKernelGGL(rope_append_kernel, grid, dim3(64), 0, stream, qkv, ldqkv, n_heads,
-                       q_start, inv_freq, rot_dim, interleaved ? 1 : 0, factor, cache, q, ldq);
-    return hipGetLastError();
+    const int mode = rot_dim % (interleaved ? 8 : 16) != 0 ? kAny : interleaved ? kInterleaved
+                                                                                : kHalf;
+    // threads a head: a power of two that covers its pieces
+    const int pieces = mode == kHalf ? (c.head_dim - rot_dim / 2) / 8 : c.head_dim / 8;
+    int shift = 0;
+    while ((1 << shift) < pieces) ++shift;
+    int threads = (n_heads + 2 * c.n_kv) << shift;
+    threads = threads >= kThreads ? kThreads : (threads + kWave - 1) / kWave * kWave;
+    const int il = interleaved ? 1 : 0;
+    if (mode == kHalf)
+        return launch<kHalf>(T, threads, stream, qkv, ldqkv, n_heads, q_start, inv_freq, rot_dim,
+                             il, factor, c, q, ldq, shift);
+    if (mode == kInterleaved)
+        return launch<kInterleaved>(T, threads, stream, qkv, ldqkv, n_heads, q_start, inv_freq,
+                                    rot_dim, il, factor, c, q, ldq, shift);
+    return launch<kAny>(T, threads, stream, qkv, ldqkv, n_heads, q_start, inv_freq, rot_dim, il,
+                        factor, c, q, ldq, shift);
 }
 
 }  // namespace w4
