@@ -187,7 +187,9 @@ size_t w4_attn_decode_work_bytes(int n_heads, const w4_kv_cache *cache, int64_t 
                                  int64_t sinks) {
     w4::KvView view;
     w4::AttnArgs a{};
-    if (check_cache(cache, n_heads, &view) || check_mask(window, sinks, view, &a)) return 0;
+    if (check_cache(cache, n_heads, &view) || check_mask(window, sinks, view, &a) ||
+        !w4::attn_decode_supported(n_heads, view))
+        return 0;
     return w4::attn_decode_work_bytes(n_heads, view, a.window, a.sinks);
 }
 
@@ -199,6 +201,7 @@ int w4_attn_decode(const uint16_t *q, int64_t ldq, int n_heads, const w4_kv_cach
     if (int st = check_attn(q, cache ? cache->n_seqs : 1, ldq, n_heads, nullptr, cache, scale,
                             window, sinks, y, ldy, out_dtype, lse, work, &view, &a))
         return st;
+    if (!w4::attn_decode_supported(n_heads, view)) return W4_ERR_RANGE;
     if (int st = check_work(w4::attn_decode_work_bytes(n_heads, view, a.window, a.sinks), work,
                             work_bytes))
         return st;

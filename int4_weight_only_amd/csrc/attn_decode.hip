@@ -12,10 +12,14 @@
 // cores have time to spare here.
 //
 // A sequence's visible keys (its sinks, then its window; all without a window) are cut into tiles
-// of 32 keys and chunks of tiles; a workgroup takes a chunk, each of its four waves every fourth
-// tile on its own (no barrier in the loop, the next tile's loads in flight), and joins the waves'
-// results in LDS. Where a sequence has more than one chunk, the chunks' results meet in the caller's
-// workspace and a second kernel joins them in order.
+// of 32 keys. The tiles of all units (sequence, key-value head, 16 query heads) stand in one line,
+// and every workgroup takes the same number of consecutive ones, so that ragged lengths leave no
+// compute unit idle; in a workgroup each of the four waves takes every fourth tile on its own (no
+// barrier in the loop, the next tile's loads in flight), and the waves join in LDS. A unit that lies
+// in more than one workgroup leaves partial sums in the caller's workspace (at most two per
+// workgroup), which a second kernel joins in order.
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace w4 {
@@ -48,264 +52,420 @@ __device__ __forceinline__ Keys visible_keys(const AttnArgs &a, const KvView &c,
     return k;
 }
 
-// Partial results: per (sequence, head, chunk) D weighted sums, then per (sequence, head, chunk)
-// the pair (maximum in log2 units, sum of weights).
-struct Partials {
-    float *o;
-    float *ml;
-    int chunks;
+// How the line of tiles is cut. whole_units: a workgroup per unit (caches so short that splitting
+// them costs more than it gives). Otherwise a workgroup takes `per` tiles, as few as `slots`
+// workgroups need, but one for each wave, or a unit's average where that is less.
+struct Plan {
+    int units_per_seq, units, slots, grid;
+    bool whole_units;
 };
+__device__ __forceinline__ int tiles_per_group(const Plan &p, int total) {
+    const int per = (total + p.slots - 1) / p.slots, avg = (total + p.units - 1) / p.units;
+    return max(per, min(avg, kWaves));
+}
 
-__host__ __device__ __forceinline__ Partials partials(void *work, int64_t pairs, int chunks,
-                                                      int D) {
-    Partials p;
-    p.o = static_cast<float *>(work);
-    p.ml = p.o + pairs * chunks * D;
-    p.chunks = chunks;
-    return p;
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Tiles of all sequences, and of those before sequence `upto`. Every lane of a wave takes part.
+// (The entry point bounds the tiles of all units by 2^31.)
+__device__ __forceinline__ void count_tiles(const AttnArgs &a, const KvView &c, int upto,
+                                            int *total, int *before) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int sum = 0, pre = 0;
+    for (int b = lane; b < c.n_seqs; b += kWave) {
+        const int n = visible_keys(a, c, b).n_tiles;
+        sum += n;
+        pre += b < upto ? n : 0;
+    }
+    *total = wave_sum_dpp(sum);
+    *before = wave_sum_dpp(pre);
+}
+
+// The sequence that holds tile `at` of the line, and the tiles of the line before it.
+__device__ __forceinline__ int find_sequence(const AttnArgs &a, const KvView &c, int at,
+                                             int units_per_seq, int *before) {
+    const int lane = threadIdx.x & (kWave - 1);
+    int base = 0;
+    for (int b0 = 0; b0 < c.n_seqs; b0 += kWave) {
+        const int mine = b0 + lane < c.n_seqs
+                             ? visible_keys(a, c, b0 + lane).n_tiles * units_per_seq
+                             : 0;
+        int sum = mine;
+#pragma unroll
+        for (int o = 1; o < kWave; o <<= 1) {
+            const int v = __shfl_up(sum, o, kWave);
+            if (lane >= o) sum += v;
+        }
+        const uint64_t hit = __ballot(base + sum > at);
+        if (hit) {
+            const int w = __builtin_ctzll(hit);
+            *before = uniform(base + __shfl(sum - mine, w, kWave));
+            return uniform(b0 + w);
+        }
+        base = uniform(base + __shfl(sum, kWave - 1, kWave));
+    }
+    *before = base;
+    return c.n_seqs;
+}
+
+// A partial result: `rows` maxima (log2 units), `rows` sums of weights, then rows x D weighted
+// sums. A workgroup has two: of the unit it begins in the middle of (or that outlasts it), and of
+// the last unit it begins.
+__device__ __forceinline__ float *partial(void *work, int64_t group, int which, int rows, int D) {
+    return static_cast<float *>(work) + (2 * group + which) * rows * (D + 2);
+}
+
+// The rows of a sequence without keys: zeros.
+__device__ __forceinline__ void write_empty(const AttnArgs &a, const KvView &c, int b) {
+    const int width = a.n_heads * c.head_dim;
+    for (int i = threadIdx.x; i < width; i += kWaves * 64)
+        store_out(a.y, b * a.ldy + i, 0.0f, a.out_f32);
+    if (a.lse)
+        for (int h = threadIdx.x; h < a.n_heads; h += kWaves * 64)
+            a.lse[static_cast<int64_t>(b) * a.n_heads + h] = -INFINITY;
 }
 
 // PAGE16: pages of 16 slots and more, so that 16 aligned keys lie in one page.
+#ifndef WPE128
+#define WPE128 3
+#endif
+#ifndef WPE256
+#define WPE256 1
+#endif
+#ifndef WHOLE
+#define WHOLE 8
+#endif
+#ifndef SL64
+#define SL64 4
+#endif
+#ifndef SL128
+#define SL128 3
+#endif
+#ifndef SL256
+#define SL256 2
+#endif
 template <int DP, bool PAGE16>
 __global__ void __launch_bounds__(kWaves * 64)
-__attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode_kernel(
-    AttnArgs a, KvView c, int chunk_tiles, Partials parts) {
+__attribute__((amdgpu_waves_per_eu(DP > 128 ? WPE256 : DP > 64 ? WPE128 : 4))) attn_decode_kernel(
+    AttnArgs a, KvView c, Plan plan) {
     constexpr int KS = DP / 32;      // steps of the first product
     constexpr int DT = DP / 16;      // tiles of the second
     constexpr int kChunks = DP / 8;  // 16-byte chunks of a row
     constexpr int kVRows = 64 / kChunks;       // rows a wave's load instruction covers
     constexpr int kVLoads = kTile / kVRows;
-    // per wave: the value tile [32][DP] bf16; after the loop its sums [16][DP] fp32 (the same size)
-    __shared__ __attribute__((aligned(16))) uint16_t sv[kWaves][kTile * DP];
+    constexpr int kRow = Rows<DP>::kValue;
+    // per wave: the value tile, 32 rows of bf16; after the loop its sums, 16 rows of fp32
+    __shared__ __attribute__((aligned(16))) uint16_t sv[kWaves][kTile * kRow];
     __shared__ float sm[kWaves][kRows], sl[kWaves][kRows];
 
-    const int lane = threadIdx.x & 63;
     const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int G = a.n_heads / c.n_kv, D = c.head_dim;
     const int row_tiles = (G + kRows - 1) / kRows;
-    int id = blockIdx.x;
-    const int rt = id % row_tiles;
-    id /= row_tiles;
-    const int hk = id % c.n_kv;
-    id /= c.n_kv;
-    const int b = id % c.n_seqs, chunk = id / c.n_seqs;
-    const Keys keys = visible_keys(a, c, b);
-    const int t0 = chunk * chunk_tiles;
-    const int t1 = min(keys.n_tiles, t0 + chunk_tiles);
-    if (chunk > 0 && t0 >= t1) return;  // (chunk 0 of an empty sequence writes its zeros)
+    const float cs = a.scale * kLog2e;
+    uint16_t *my_v = sv[wid];
 
-    const int r = lane & 15, g = lane >> 4;  // column (query head), group of 16 lanes
-    const int head0 = hk * G + rt * kRows;
-    const int n_rows = min(G - rt * kRows, kRows);
-
-    bf16x8_t qf[KS];
-    {
-        const uint16_t *src = a.q + b * a.ldq + static_cast<int64_t>(head0 + min(r, n_rows - 1)) * D;
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            const int d = 32 * s + 8 * g;
-            uintx4_t v = {0, 0, 0, 0};
-            if (d < D) v = *reinterpret_cast<const uintx4_t *>(src + d);
-            qf[s] = __builtin_bit_cast(bf16x8_t, v);
-        }
+    // this workgroup's tiles of the line: line0 .. line1
+    int line0, line1, seq_begin, b;
+    if (plan.whole_units) {
+        b = blockIdx.x / plan.units_per_seq;
+        const int n = visible_keys(a, c, b).n_tiles;
+        seq_begin = 0;
+        line0 = static_cast<int>(blockIdx.x % plan.units_per_seq) * n;
+        line1 = line0 + n;
+    } else {
+        int total, unused;
+        count_tiles(a, c, 0, &total, &unused);
+        total *= plan.units_per_seq;
+        const int per = tiles_per_group(plan, total);
+        line0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * per,
+                                     static_cast<int64_t>(total)));
+        line1 = min(line0 + per, total);
+        b = find_sequence(a, c, line0, plan.units_per_seq, &seq_begin);
     }
+    // A sequence without keys has no tile: its rows are written by the group of its number.
+    for (int e = blockIdx.x; e < c.n_seqs; e += gridDim.x)
+        if (kv_length(c, e) == 0) write_empty(a, c, e);
 
-    const int32_t *table = c.table + b * c.ld_table;
-    const int64_t head_off = static_cast<int64_t>(hk) * c.head_stride;
-    const auto visible = [&](int p) { return p <= keys.last && (p >= keys.lo || p < a.sinks); };
-    // Where the 16 keys from s0 on are read: a key that is not visible is replaced by one that is
-    // (finite values; its weight is 0), by one of the same 16 if there is any.
-    const auto safe_key = [&](int s0) {
-        if (s0 <= keys.last && (s0 < a.sinks || s0 + 15 >= keys.lo))
-            return s0 < a.sinks && s0 < keys.lo ? s0 : max(s0, keys.lo);
-        return keys.last;
-    };
-    // Element offset of key p of the 16 from s0 on (page_off: the offset of safe_key(s0)'s page).
-    const auto page_off = [&](int safe) {
-        return static_cast<int64_t>(kv_page(c, table, safe)) * c.page_stride + head_off;
-    };
-    const auto in_page = [&](int p, int safe) {
-        return static_cast<uint32_t>(((visible(p) ? p : safe) & c.page_mask) * c.slot_stride);
-    };
+    for (int at = line0; at < line1;) {
+        // (an opaque copy: addresses made from it are computed here for each unit, rather than kept
+        // in registers through all of them)
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int lane = tid & 63;
+        const int r = lane & 15, g = lane >> 4;  // column (query head), group of 16 lanes
+        b = uniform(b);
+        const Keys keys = visible_keys(a, c, b);
+        if (keys.n_tiles == 0) {
+            ++b;
+            continue;
+        }
+        const int unit = uniform((at - seq_begin) / keys.n_tiles);
+        if (unit >= plan.units_per_seq) {  // the sequence is done
+            seq_begin += keys.n_tiles * plan.units_per_seq;
+            ++b;
+            continue;
+        }
+        const int unit_begin = seq_begin + unit * keys.n_tiles;
+        const int t0 = uniform(at - unit_begin);
+        const int t1 = uniform(min(line1 - unit_begin, keys.n_tiles));
+        const int rt = unit % row_tiles, hk = unit / row_tiles;
+        const int head0 = hk * G + rt * kRows;
+        const int n_rows = min(G - rt * kRows, kRows);
 
-    uintx4_t rk[2][KS], rv[kVLoads];
-    const auto fetch_k = [&](int k0) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int s0 = k0 + 16 * u, safe = safe_key(s0), p = s0 + r;
-            const uint16_t *row = c.k + (PAGE16 ? page_off(safe)
-                                                : page_off(visible(p) ? p : safe)) +
-                                  in_page(p, safe);
+        bf16x8_t qf[KS];
+        {
+            const uint16_t *src = a.q + b * a.ldq + static_cast<int64_t>(head0 + min(r, n_rows - 1)) * D;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const int d = 32 * s + 8 * g;
-                rk[u][s] = uintx4_t{0, 0, 0, 0};
-                if (d < D) rk[u][s] = *reinterpret_cast<const uintx4_t *>(row + d);
+                const uintx4_t v = *reinterpret_cast<const uintx4_t *>(src + min(d, D - 8));
+                qf[s] = __builtin_bit_cast(bf16x8_t, d < D ? v : uintx4_t{0, 0, 0, 0});
             }
         }
-    };
-    const int v_row = lane / kChunks, v_chunk = lane % kChunks;
-    const auto fetch_v = [&](int k0) {
-#pragma unroll
-        for (int i = 0; i < kVLoads; ++i) {
-            const int s0 = k0 + i * kVRows / 16 * 16, safe = safe_key(s0);
-            const int p = k0 + i * kVRows + v_row;
-            rv[i] = uintx4_t{0, 0, 0, 0};
-            if (v_chunk * 8 < D)
-                rv[i] = *reinterpret_cast<const uintx4_t *>(
-                    c.v + (PAGE16 ? page_off(safe) : page_off(visible(p) ? p : safe)) +
-                    in_page(p, safe) + v_chunk * 8);
-        }
-    };
 
-    floatx4_t o[DT];
-#pragma unroll
-    for (int i = 0; i < DT; ++i) o[i] = floatx4_t(0.0f);
-    const float cs = a.scale * kLog2e;
-    float M = kNoMax, l = 0.0f;
-    uint16_t *my_v = sv[wid];
+        const int32_t *table = c.table + b * c.ld_table;
+        const int64_t head_off = static_cast<int64_t>(hk) * c.head_stride;
+        const auto visible = [&](int p) { return p <= keys.last && (p >= keys.lo || p < a.sinks); };
+        // 16 keys as they are read: the page offset of a visible key among them (of the newest key if
+        // there is none), and that key. Keys that are not visible are read from it: finite values,
+        // whose weight is 0.
+        struct Span {
+            int start, safe;
+            int64_t page;
+        };
+        const auto safe_key = [&](int s0) {
+            if (s0 < a.sinks && s0 < keys.lo) return s0;
+            return s0 > keys.last || s0 + 15 < keys.lo ? keys.last : max(s0, keys.lo);
+        };
+        const auto page_offset = [&](int page) {
+            page = page < 0 ? 0 : (page >= c.n_pages ? c.n_pages - 1 : page);
+            return static_cast<int64_t>(page) * c.page_stride + head_off;
+        };
+        // Eight elements from element `col` on of row i (0..15) of a span. (The page's address is
+        // uniform where the span lies in one page: a scalar base and a 32-bit offset in bytes.)
+        const auto load_row = [&](const uint16_t *kv, const Span &sp, int i, int col) {
+            const int p = sp.start + i;
+            const int from = visible(p) ? p : sp.safe;
+            const int64_t page =
+                PAGE16 ? sp.page : page_offset(read_const(table + (from >> c.page_shift)));
+            const uint32_t off = (from & c.page_mask) * c.slot_stride + col;
+            return *reinterpret_cast<const uintx4_t *>(
+                reinterpret_cast<const char *>(kv + page) + 2u * off);
+        };
 
-    int t = t0 + wid;
-    if (t < t1) {
-        fetch_k(keys.start(t));
-        fetch_v(keys.start(t));
-    }
-    for (; t < t1; t += kWaves) {
-        const int k0 = keys.start(t);
-        const int next = keys.start(min(t + kWaves, t1 - 1));  // (the last tile again at the end)
-        floatx4_t s[2];
+        // The next tile to be fetched, and the one after it: their spans' keys, and the table entries
+        // on their way.
+        Span next[2];
+        int entry[2] = {0, 0};
+        const auto look_up = [&](int t) {
+            if (!PAGE16) return;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            s[u] = floatx4_t(0.0f);
+            for (int u = 0; u < 2; ++u)
+                entry[u] = read_const(table + (safe_key(keys.start(t) + 16 * u) >> c.page_shift));
+        };
+        const auto locate = [&](int t) {
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-                s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                    __builtin_bit_cast(bf16x8_t, rk[u][ks]), qf[ks], s[u], 0, 0, 0);
-        }
-        fetch_k(next);
-#pragma unroll
-        for (int i = 0; i < kVLoads; ++i)
-            *reinterpret_cast<uintx4_t *>(
-                &my_v[8 * value_slot<DP>(i * kVRows + v_row, v_chunk)]) = rv[i];
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
-        fetch_v(next);
-
-        float mx = -INFINITY;
-        bool ok[2][4];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ok[u][i] = visible(k0 + 16 * u + 4 * g + i);
-                s[u][i] = s[u][i] * cs;
-                mx = ok[u][i] ? fmaxf(mx, s[u][i]) : mx;
+            for (int u = 0; u < 2; ++u) {
+                next[u].start = keys.start(t) + 16 * u;
+                next[u].safe = safe_key(next[u].start);
+                next[u].page = page_offset(entry[u]);
             }
-        mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
-        mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-        if (__any(mx > M + kSlack)) {
-            const float M2 = fmaxf(M, mx);
-            const float f = __builtin_amdgcn_exp2f(M - M2);
-            M = M2;
-            l *= f;
+        };
+        // Dims past D repeat the row's last chunk: they meet zeros of q, or outputs that are not kept.
+        const int v_row = lane / kChunks, v_chunk = min(8 * (lane % kChunks), D - 8);
+        uintx4_t rk[2][KS], rv[kVLoads];
+        const auto fetch_k = [&] {
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] *= f;
-        }
-        uintx4_t hi, lo;
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+                for (int s = 0; s < KS; ++s)
+                    rk[u][s] = load_row(c.k, next[u], r, min(32 * s + 8 * g, D - 8));
+        };
+        const auto fetch_v = [&] {
 #pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const float p0 = ok[u][i] ? __builtin_amdgcn_exp2f(s[u][i] - M) : 0.0f;
-                const float p1 = ok[u][i + 1] ? __builtin_amdgcn_exp2f(s[u][i + 1] - M) : 0.0f;
-                l += p0 + p1;
-                const uint32_t w = pack_bf16(p0, p1);
-                hi[2 * u + i / 2] = w;
-                lo[2 * u + i / 2] = pack_bf16(p0 - __uint_as_float(w << 16),
-                                              p1 - __uint_as_float(w & 0xFFFF0000u));
-            }
-        // slots 8 g + 0..3 are keys 4 g + 0..3, slots 8 g + 4..7 keys 16 + 4 g + 0..3
-        const int vr = 4 * g + r / 4;
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            const int col = 16 * d + 4 * (r & 3);
-            const uintx2_t v0 = lds_read_transposed(&my_v[8 * value_slot<DP>(vr, col / 8) + col % 8]);
-            const uintx2_t v1 =
-                lds_read_transposed(&my_v[8 * value_slot<DP>(vr + 16, col / 8) + col % 8]);
-            const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
-            const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vv);
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8_t, hi),
-                                                           o[d], 0, 0, 0);
-            o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8_t, lo),
-                                                           o[d], 0, 0, 0);
-        }
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_wave_barrier();
-    }
+            for (int i = 0; i < kVLoads; ++i)
+                rv[i] = load_row(c.v, next[i * kVRows / 16], i * kVRows % 16 + v_row, v_chunk);
+        };
 
-    // Join the waves: lane (g, r) holds dims 16 d + 4 g + 0..3 of head r.
-    l += __shfl_xor(l, 16, kWave);
-    l += __shfl_xor(l, 32, kWave);
-    if (g == 0) {
-        sm[wid][r] = M;
-        sl[wid][r] = l;
-    }
-    float *my_o = reinterpret_cast<float *>(my_v);
+        floatx4_t o[DT];
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
-        *reinterpret_cast<floatx4_t *>(&my_o[r * DP + 16 * d + 4 * g]) = o[d];
-    __syncthreads();
-    const bool whole = keys.n_tiles <= chunk_tiles;  // this chunk is all there is
-    const bool wide = wide_rows(a);
-    for (int e = threadIdx.x; e < n_rows * (DP / 4); e += kWaves * 64) {
-        const int row = e / (DP / 4), d = e % (DP / 4) * 4;
-        if (d >= D) continue;
-        float m = sm[0][row], sum = 0.0f;
+        for (int i = 0; i < DT; ++i) o[i] = floatx4_t(0.0f);
+        float M = kNoMax, l = 0.0f;
+
+        // One tile; with MORE, the wave's next tile is fetched on the way, and the one after that
+        // looked up.
+        const auto step = [&](auto more, int t) {
+            constexpr bool MORE = decltype(more)::value;
+            const int k0 = keys.start(t), after = min(t + 2 * kWaves, t1 - 1);
+            if constexpr (MORE) look_up(after);
+            floatx4_t s[2];
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w][row]);
-        floatx4_t v = floatx4_t(0.0f);
+            for (int u = 0; u < 2; ++u) {
+                s[u] = floatx4_t(0.0f);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
-            const float f = __builtin_amdgcn_exp2f(sm[w][row] - m);
-            sum += f * sl[w][row];
-            v += f * *reinterpret_cast<const floatx4_t *>(
-                         reinterpret_cast<const float *>(sv[w]) + row * DP + d);
+                for (int ks = 0; ks < KS; ++ks)
+                    s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8_t, rk[u][ks]), qf[ks], s[u], 0, 0, 0);
+            }
+            phase_fence();
+            if constexpr (MORE) fetch_k();
+            phase_fence();
+#pragma unroll
+            for (int i = 0; i < kVLoads; ++i)
+                *reinterpret_cast<uintx4_t *>(
+                    &my_v[(i * kVRows + v_row) * kRow + 8 * (lane % kChunks)]) = rv[i];
+            phase_fence();
+            __builtin_amdgcn_wave_barrier();
+            if constexpr (MORE) {
+                fetch_v();
+                locate(after);
+            }
+            phase_fence();
+
+            float mx = -INFINITY;
+            bool ok[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ok[u][i] = visible(k0 + 16 * u + 4 * g + i);
+                    s[u][i] = s[u][i] * cs;
+                    mx = ok[u][i] ? fmaxf(mx, s[u][i]) : mx;
+                }
+            mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
+            mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
+            if (__any(mx > M + kSlack)) {
+                const float M2 = fmaxf(M, mx);
+                const float f = __builtin_amdgcn_exp2f(M - M2);
+                M = M2;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[d] *= f;
+            }
+            uintx4_t hi, lo;
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float p0 = ok[u][i] ? __builtin_amdgcn_exp2f(s[u][i] - M) : 0.0f;
+                    const float p1 = ok[u][i + 1] ? __builtin_amdgcn_exp2f(s[u][i + 1] - M) : 0.0f;
+                    l += p0 + p1;
+                    const uint32_t w = pack_bf16(p0, p1);
+                    hi[2 * u + i / 2] = w;
+                    lo[2 * u + i / 2] = pack_bf16(p0 - __uint_as_float(w << 16),
+                                                  p1 - __uint_as_float(w & 0xFFFF0000u));
+                }
+            // slots 8 g + 0..3 are keys 4 g + 0..3, slots 8 g + 4..7 keys 16 + 4 g + 0..3
+            const uint16_t *vp = &my_v[(4 * g + r / 4) * kRow + 4 * (r & 3)];
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const uintx2_t v0 = lds_read_transposed(vp + 16 * d);
+                const uintx2_t v1 = lds_read_transposed(vp + 16 * kRow + 16 * d);
+                const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
+                const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vv);
+                o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8_t, hi),
+                                                               o[d], 0, 0, 0);
+                o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8_t, lo),
+                                                               o[d], 0, 0, 0);
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+        };
+        int t = t0 + wid;
+        if (t < t1) {
+            look_up(t);
+            locate(t);
+            fetch_k();
+            fetch_v();
+            look_up(min(t + kWaves, t1 - 1));
+            locate(min(t + kWaves, t1 - 1));
+            if (t + kWaves < t1) {
+                do {
+                    step(std::true_type{}, t);
+                    t += kWaves;
+                } while (t + kWaves < t1);
+            }
+            step(std::false_type{}, t);
         }
-        const int64_t pair = static_cast<int64_t>(b) * a.n_heads + head0 + row;
-        if (whole) {
-            v *= sum > 0.0f ? 1.0f / sum : 0.0f;
-            store_out4(a.y, b * a.ldy + static_cast<int64_t>(head0 + row) * D + d, v, a.out_f32,
-                       wide);
-            if (a.lse && d == 0) a.lse[pair] = sum > 0.0f ? m * kLn2 + logf(sum) : -INFINITY;
-        } else {
-            const int64_t at = pair * parts.chunks + chunk;
-            *reinterpret_cast<floatx4_t *>(parts.o + at * D + d) = v;
-            if (d == 0) {
-                parts.ml[2 * at] = m;
-                parts.ml[2 * at + 1] = sum;
+
+        // Join the waves: lane (g, r) holds dims 16 d + 4 g + 0..3 of head r.
+        l += __shfl_xor(l, 16, kWave);
+        l += __shfl_xor(l, 32, kWave);
+        if (g == 0) {
+            sm[wid][r] = M;
+            sl[wid][r] = l;
+        }
+        float *my_o = reinterpret_cast<float *>(my_v);
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+            *reinterpret_cast<floatx4_t *>(&my_o[r * kRow + 16 * d + 4 * g]) = o[d];
+        __syncthreads();
+        const bool whole = t0 == 0 && t1 == keys.n_tiles;
+        const bool wide = wide_rows(a);
+        const int slot_rows = min(G, kRows);
+        float *part = partial(a.work, blockIdx.x, at == line0 ? 0 : 1, slot_rows, D);
+        for (int e = tid; e < n_rows * (DP / 4); e += kWaves * 64) {
+            const int row = e / (DP / 4), d = e % (DP / 4) * 4;
+            if (d >= D) continue;
+            float m = sm[0][row], sum = 0.0f;
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w][row]);
+            floatx4_t v = floatx4_t(0.0f);
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                const float f = __builtin_amdgcn_exp2f(sm[w][row] - m);
+                sum += f * sl[w][row];
+                v += f * *reinterpret_cast<const floatx4_t *>(
+                             reinterpret_cast<const float *>(sv[w]) + row * kRow + d);
+            }
+            if (whole) {
+                v *= sum > 0.0f ? 1.0f / sum : 0.0f;
+                store_out4(a.y, b * a.ldy + static_cast<int64_t>(head0 + row) * D + d, v, a.out_f32,
+                           wide);
+                if (a.lse && d == 0)
+                    a.lse[static_cast<int64_t>(b) * a.n_heads + head0 + row] =
+                        sum > 0.0f ? m * kLn2 + logf(sum) : -INFINITY;
+            } else {
+                *reinterpret_cast<floatx4_t *>(part + 2 * slot_rows + row * D + d) = v;
+                if (d == 0) {
+                    part[row] = m;
+                    part[slot_rows + row] = sum;
+                }
             }
         }
+        at = unit_begin + t1;
+        if (at < line1) __syncthreads();  // before the next unit's values overwrite the sums
     }
 }
 
-// Joins a (sequence, head)'s chunks: one workgroup each, its threads over groups of chunks and the
-// head's dims, the groups' sums through LDS in order.
+// Joins the partial results of a (sequence, head): one workgroup each, its threads over groups of
+// partials and the head's dims, the groups' sums through LDS in order.
 constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvView c,
-                                                                 int chunk_tiles, Partials parts) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvView c, Plan plan) {
     __shared__ floatx4_t so[kJoinThreads];
     __shared__ float red[kJoinThreads / 64], sw[kJoinThreads];
     const int64_t pair = blockIdx.x;
     const int b = static_cast<int>(pair / a.n_heads), head = static_cast<int>(pair % a.n_heads);
+    const int G = a.n_heads / c.n_kv, D = c.head_dim, rows = min(G, kRows);
     const int n_tiles = visible_keys(a, c, b).n_tiles;
-    if (n_tiles <= chunk_tiles) return;  // written by the first kernel
-    const int n = (n_tiles + chunk_tiles - 1) / chunk_tiles;
-    const float *ml = parts.ml + 2 * pair * parts.chunks;
-    const float *o = parts.o + pair * parts.chunks * c.head_dim;
+    if (n_tiles == 0) return;
+    int total, before;
+    count_tiles(a, c, b, &total, &before);
+    const int per = tiles_per_group(plan, total * plan.units_per_seq);
+    const int row_tiles = (G + kRows - 1) / kRows, in_group = head % G;
+    const int unit = head / G * row_tiles + in_group / kRows, row = in_group % kRows;
+    const int u0 = before * plan.units_per_seq + unit * n_tiles;
+    const int g0 = u0 / per, g1 = (u0 + n_tiles - 1) / per;
+    if (g0 == g1) return;  // written by the first kernel
+    const int n = g1 - g0 + 1;
+    // the unit is the last that its first group begins, unless it begins with the group
+    const auto part = [&](int i) {
+        return partial(a.work, g0 + i, i == 0 && u0 % per != 0 ? 1 : 0, rows, D);
+    };
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
 
     float m = kNoMax;
-    for (int i = tid; i < n; i += kJoinThreads) m = fmaxf(m, ml[2 * i]);
+    for (int i = tid; i < n; i += kJoinThreads) m = fmaxf(m, part(i)[row]);
     m = wave_max(m);
     if (lane == 0) red[wid] = m;
     __syncthreads();
@@ -313,16 +473,17 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvV
 #pragma unroll
     for (int w = 1; w < kJoinThreads / 64; ++w) m = fmaxf(m, red[w]);
 
-    const int lanes = c.head_dim / 4;          // threads over the dims, 4 each
-    const int groups = kJoinThreads / lanes;   // (threads past groups * lanes idle)
+    const int lanes = D / 4;                  // threads over the dims, 4 each
+    const int groups = kJoinThreads / lanes;  // (threads past groups * lanes idle)
     const int grp = tid / lanes, d = tid % lanes * 4;
     float l = 0.0f;
     floatx4_t v = floatx4_t(0.0f);
     if (grp < groups) {
         for (int i = grp; i < n; i += groups) {
-            const float f = __builtin_amdgcn_exp2f(ml[2 * i] - m);
-            l += f * ml[2 * i + 1];
-            v += f * *reinterpret_cast<const floatx4_t *>(o + static_cast<int64_t>(i) * c.head_dim + d);
+            const float *p = part(i);
+            const float f = __builtin_amdgcn_exp2f(p[row] - m);
+            l += f * p[rows + row];
+            v += f * *reinterpret_cast<const floatx4_t *>(p + 2 * rows + row * D + d);
         }
         so[tid] = v;
         sw[tid] = l;
@@ -334,68 +495,69 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvV
         l += sw[q * lanes + tid];
     }
     v *= l > 0.0f ? 1.0f / l : 0.0f;
-    store_out4(a.y, b * a.ldy + static_cast<int64_t>(head) * c.head_dim + d, v, a.out_f32,
-               wide_rows(a));
+    store_out4(a.y, b * a.ldy + static_cast<int64_t>(head) * D + d, v, a.out_f32, wide_rows(a));
     if (a.lse && d == 0) a.lse[pair] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
-// How the keys are cut: chunks of at least one tile per wave, as few as give the card four
-// workgroups per compute unit.
-struct Plan {
-    int chunk_tiles, chunks, units;
-};
 Plan plan_of(int n_heads, const KvView &c, int window, int sinks) {
     const int G = n_heads / c.n_kv;
     Plan p;
-    p.units = c.n_seqs * c.n_kv * ((G + kRows - 1) / kRows);
+    p.units_per_seq = c.n_kv * ((G + kRows - 1) / kRows);
+    p.units = c.n_seqs * p.units_per_seq;
     // tiles a sequence can have: its window and its sinks touch at most two partial tiles each
     int64_t keys = c.capacity;
     if (window > 0 && int64_t(window) + sinks + 4 * kTile < keys)
         keys = int64_t(window) + sinks + 4 * kTile;
     const int64_t tiles = (keys + kTile - 1) / kTile;
-    const int64_t want = 4ll * device_cu_count();
-    int64_t per = (tiles * p.units + want - 1) / want;
-    per = (per + kWaves - 1) / kWaves * kWaves;
-    p.chunk_tiles = static_cast<int>(per < kWaves ? kWaves : per);
-    p.chunks = static_cast<int>((tiles + p.chunk_tiles - 1) / p.chunk_tiles);
+    p.whole_units = tiles <= WHOLE;
+    p.slots = device_cu_count() * (c.head_dim > 128 ? SL256 : c.head_dim > 64 ? SL128 : SL64);
+    // no more groups than tiles_per_group can make of the most tiles there can be
+    const int64_t most = (tiles * p.units + kWaves - 1) / kWaves;
+    int64_t grid = p.slots < most ? p.slots : most;
+    if (p.whole_units || grid < p.units) grid = p.units;
+    p.grid = static_cast<int>(grid);
     return p;
 }
 
 template <int DP>
-void launch(const Plan &p, const AttnArgs &a, const KvView &c, const Partials &parts,
-            hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(p.units) * static_cast<unsigned>(p.chunks));
+void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(p.grid));
     if (c.page_mask >= 15)
         hipLaunchKernelGGL((attn_decode_kernel<DP, true>), grid, dim3(kWaves * 64), 0, stream, a,
-                           c, p.chunk_tiles, parts);
+                           c, p);
     else
         hipLaunchKernelGGL((attn_decode_kernel<DP, false>), grid, dim3(kWaves * 64), 0, stream, a,
-                           c, p.chunk_tiles, parts);
+                           c, p);
 }
 
 }  // namespace
 
+bool attn_decode_supported(int n_heads, const KvView &c) {
+    const int64_t units = static_cast<int64_t>(c.n_seqs) * n_heads;  // at least
+    return units <= INT32_MAX / (c.capacity / kTile + 1);
+}
+
 size_t attn_decode_work_bytes(int n_heads, const KvView &c, int window, int sinks) {
     const Plan p = plan_of(n_heads, c, window, sinks);
-    if (p.chunks <= 1) return 0;
-    return static_cast<size_t>(c.n_seqs) * n_heads * p.chunks * (c.head_dim + 2) * sizeof(float);
+    const int G = n_heads / c.n_kv;
+    if (p.whole_units) return 0;
+    return sizeof(float) * 2 * p.grid * (G < kRows ? G : kRows) * (c.head_dim + 2);
 }
 
 hipError_t launch_attn_decode(const AttnArgs &a, const KvView &c, hipStream_t stream) {
     const Plan p = plan_of(a.n_heads, c, a.window, a.sinks);
-    const int64_t pairs = static_cast<int64_t>(c.n_seqs) * a.n_heads;
-    const Partials parts = partials(a.work, pairs, p.chunks, c.head_dim);
     if (c.head_dim <= 64)
-        launch<64>(p, a, c, parts, stream);
+        launch<64>(p, a, c, stream);
     else if (c.head_dim <= 128)
-        launch<128>(p, a, c, parts, stream);
+        launch<128>(p, a, c, stream);
     else
-        launch<256>(p, a, c, parts, stream);
-    if (p.chunks > 1) {
+        launch<256>(p, a, c, stream);
+    if (!p.whole_units) {
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
-        hipLaunchKernelGGL(attn_join_kernel, dim3(static_cast<unsigned>(pairs)),
-                           dim3(kJoinThreads), 0, stream, a, c, p.chunk_tiles, parts);
+        hipLaunchKernelGGL(attn_join_kernel,
+                           dim3(static_cast<unsigned>(c.n_seqs) * static_cast<unsigned>(a.n_heads)),
+                           dim3(kJoinThreads), 0, stream, a, c, p);
     }
     return hipGetLastError();
 }

@@ -35,24 +35,14 @@ __device__ __forceinline__ uintx2_t lds_read_transposed(const uint16_t *p) {
                               __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p)));
 }
 
-// Index (in 16-byte chunks) of chunk c of row r in a tile of rows of DP bf16, swizzled against bank
-// conflicts (64 banks of 4 bytes, 16 chunks wide).
-//   keys:   a fragment reads one chunk of 16 or 32 consecutive rows, a store one row: the chunk
-//           number is xor-ed with the row's, counted in rows of 256 bytes.
-//   values: a transposed read takes a pair of chunks of 4 consecutive rows at once: xor-ed with
-//           twice the row, which keeps the pair together.
+// Rows of a tile in LDS are DP elements and a gap, against bank conflicts (64 banks of 4 bytes), with
+// every access at a constant offset from one address per lane:
+//   keys:   a fragment reads the same 16 bytes of 16 or 32 consecutive rows: 16 bytes further each
+//   values: a transposed read takes 32 bytes of 4 consecutive rows at once: 32 bytes further each
 template <int DP>
-__device__ __forceinline__ int key_slot(int r, int c) {
-    constexpr int kChunks = DP / 8;
-    if constexpr (kChunks >= 16) return r * kChunks + (c ^ (r & 15));
-    else return r * kChunks + (c ^ ((r >> 1) & (kChunks - 1)));
-}
-template <int DP>
-__device__ __forceinline__ int value_slot(int r, int c) {
-    constexpr int kChunks = DP / 8;
-    if constexpr (kChunks >= 16) return r * kChunks + (c ^ (2 * (r & 7)));
-    else return r * kChunks + (c ^ (2 * (r & 3)));
-}
+struct Rows {
+    static constexpr int kKey = DP + 8, kValue = DP + 16;  // elements from row to row
+};
 
 // Four consecutive elements of an output row, from element idx (a multiple of 4) on. `wide`: the
 // output's base and rows allow one store.

@@ -40,8 +40,8 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
         const int b = base + lane;
         int begin = 0, end = 0;
         if (b < c.n_seqs) {
-            begin = max(q_start[b], 0);
-            end = min(q_start[b + 1], static_cast<int>(T));
+            begin = max(read_const(q_start + b), 0);
+            end = min(read_const(q_start + b + 1), static_cast<int>(T));
         }
         const int nq = max(end - begin, 0);
         const int mine = static_cast<int>((static_cast<int64_t>(nq) * G + BM - 1) / BM);
@@ -77,9 +77,10 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     constexpr int kLoads = KT * kChunks / kThreads;  // 16-byte chunks a thread stages of K, of V
     static_assert(KT * kChunks % kThreads == 0, "every thread stages the same number of chunks");
     constexpr int kRowStep = kThreads / kChunks;  // rows between a thread's chunks
+    constexpr int kKeyRow = Rows<DP>::kKey, kValueRow = Rows<DP>::kValue;
     constexpr int DT = DP / 32, KS = DP / 16, SUB = KT / 32;
-    __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * DP];
-    __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * DP];
+    __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * kKeyRow];
+    __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * kValueRow];
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -115,9 +116,8 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
             const int d = 16 * s + 8 * half;
-            uintx4_t v = {0, 0, 0, 0};
-            if (d < D) v = *reinterpret_cast<const uintx4_t *>(src + d);
-            qf[s] = __builtin_bit_cast(bf16x8_t, v);
+            const uintx4_t v = *reinterpret_cast<const uintx4_t *>(src + min(d, D - 8));
+            qf[s] = __builtin_bit_cast(bf16x8_t, d < D ? v : uintx4_t{0, 0, 0, 0});
         }
     }
 
@@ -158,8 +158,8 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int r = r0 + i * kRowStep;
-            *reinterpret_cast<uintx4_t *>(&sk[buf][8 * key_slot<DP>(r, my_chunk)]) = rk[i];
-            *reinterpret_cast<uintx4_t *>(&sv[buf][8 * value_slot<DP>(r, my_chunk)]) = rv[i];
+            *reinterpret_cast<uintx4_t *>(&sk[buf][r * kKeyRow + 8 * my_chunk]) = rk[i];
+            *reinterpret_cast<uintx4_t *>(&sv[buf][r * kValueRow + 8 * my_chunk]) = rv[i];
         }
     };
     if (n_iter > 0) {
@@ -188,7 +188,7 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
                     const bf16x8_t kf = *reinterpret_cast<const bf16x8_t *>(
-                        &sk[buf][8 * key_slot<DP>(32 * u + (lane & 31), 2 * ks + half)]);
+                        &sk[buf][(32 * u + (lane & 31)) * kKeyRow + 16 * ks + 8 * half]);
                     s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[u], 0, 0, 0);
                 }
             }
@@ -249,14 +249,13 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
                 for (int st = 0; st < 2; ++st) {
-                    const int r = 32 * u + 16 * st + 4 * half + (lane & 15) / 4;
+                    const uint16_t *vp =
+                        &sv[buf][(32 * u + 16 * st + 4 * half + (lane & 15) / 4) * kValueRow +
+                                 (lane & 16) + 4 * (lane & 3)];
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
-                        const int col = 32 * d + (lane & 16) + 4 * (lane & 3);
-                        const uintx2_t v0 = lds_read_transposed(
-                            &sv[buf][8 * value_slot<DP>(r, col / 8) + col % 8]);
-                        const uintx2_t v1 = lds_read_transposed(
-                            &sv[buf][8 * value_slot<DP>(r + 8, col / 8) + col % 8]);
+                        const uintx2_t v0 = lds_read_transposed(vp + 32 * d);
+                        const uintx2_t v1 = lds_read_transposed(vp + 8 * kValueRow + 32 * d);
                         const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
                         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                             __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);

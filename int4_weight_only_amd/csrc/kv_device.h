@@ -22,16 +22,23 @@ struct KvView {
 
 #if defined(__HIPCC__)
 
+// An element of an array that nothing writes while the kernel runs (page tables, lengths): a scalar
+// load where the address is uniform, whatever the kernel stores elsewhere.
+__device__ __forceinline__ int32_t read_const(const int32_t *p) {
+    typedef const __attribute__((address_space(4))) int32_t *const_ptr;
+    return *reinterpret_cast<const_ptr>(reinterpret_cast<uintptr_t>(p));
+}
+
 // Keys of sequence b; a length outside what its page table can hold is cut to it.
 __device__ __forceinline__ int kv_length(const KvView &c, int b) {
-    const int n = c.kv_len[b];
+    const int n = read_const(c.kv_len + b);
     return n < 0 ? 0 : (n > c.capacity ? c.capacity : n);
 }
 
 // Page that holds position pos (0 <= pos < capacity) of the sequence whose table row is `row`.
 // An entry outside the cache is moved into it, so that no entry makes an access leave the cache.
 __device__ __forceinline__ int kv_page(const KvView &c, const int32_t *row, int pos) {
-    const int p = row[pos >> c.page_shift];
+    const int p = read_const(row + (pos >> c.page_shift));
     return p < 0 ? 0 : (p >= c.n_pages ? c.n_pages - 1 : p);
 }
 
@@ -60,13 +67,13 @@ __device__ __forceinline__ bool place_of_row(const KvView &c, const int32_t *q_s
     int lo = 0, hi = c.n_seqs - 1;  // the last sequence that starts at or before t
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (q_start[mid] <= t)
+        if (read_const(q_start + mid) <= t)
             lo = mid;
         else
             hi = mid - 1;
     }
-    const int end = q_start[lo + 1];
-    if (t < q_start[lo] || t >= end) return false;
+    const int end = read_const(q_start + lo + 1);
+    if (t < read_const(q_start + lo) || t >= end) return false;
     r->seq = lo;
     r->n_keys = kv_length(c, lo);
     r->pos = r->n_keys - (end - t);

@@ -153,6 +153,7 @@ struct AttnArgs {
     float *lse;
     void *work;
 };
+bool attn_decode_supported(int n_heads, const KvView &cache);  // the sizes it counts in 31 bits
 size_t attn_decode_work_bytes(int n_heads, const KvView &cache, int window, int sinks);
 hipError_t launch_attn_decode(const AttnArgs &a, const KvView &cache, hipStream_t stream);
 size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &cache, int window, int sinks);
