@@ -12,12 +12,12 @@
 // cores have time to spare here.
 //
 // A sequence's visible keys (its sinks, then its window; all without a window) are cut into tiles
-// of 32 keys. The tiles of all units (sequence, key-value head, 16 query heads) stand in one line,
-// and every workgroup takes the same number of consecutive ones, so that ragged lengths leave no
-// compute unit idle; in a workgroup each of the four waves takes every fourth tile on its own (no
-// barrier in the loop, the next tile's loads in flight), and the waves join in LDS. A unit that lies
-// in more than one workgroup leaves partial sums in the caller's workspace (at most two per
-// workgroup), which a second kernel joins in order.
+// of 32 keys. Every unit (sequence, key-value head, 16 query heads) is cut into equal shares of at
+// most `per` tiles, a workgroup each, `per` being such that the shares of all sequences together fill
+// the card once: ragged lengths leave no compute unit idle. In a workgroup each of the four waves
+// takes every fourth tile on its own (no barrier in the loop, the next tile's loads in flight), and
+// the waves join in LDS. The shares of a unit that was cut meet in the caller's workspace, and a
+// second kernel joins them in order.
 #include <type_traits>
 
 #include "attn_device.h"
@@ -41,9 +41,8 @@ struct Keys {
     }
 };
 
-__device__ __forceinline__ Keys visible_keys(const AttnArgs &a, const KvView &c, int b) {
+__device__ __forceinline__ Keys visible_keys(const AttnArgs &a, int n) {  // of n keys
     Keys k;
-    const int n = kv_length(c, b);
     k.last = n - 1;
     k.lo = a.window > 0 ? max(n - a.window, 0) : 0;
     k.n_sink = (min(a.sinks, k.lo) + kTile - 1) / kTile;
@@ -51,68 +50,69 @@ __device__ __forceinline__ Keys visible_keys(const AttnArgs &a, const KvView &c,
     k.n_tiles = n == 0 ? 0 : k.n_sink + k.last / kTile + 1 - k.lo_tile;
     return k;
 }
+__device__ __forceinline__ Keys visible_keys(const AttnArgs &a, const KvView &c, int b) {
+    return visible_keys(a, kv_length(c, b));
+}
 
-// How the line of tiles is cut. whole_units: a workgroup per unit (caches so short that splitting
-// them costs more than it gives). Otherwise a workgroup takes `per` tiles, as few as `slots`
-// workgroups need, but one for each wave, or a unit's average where that is less.
+// How the tiles are shared out. whole_units: one share per unit (caches so short that cutting them
+// costs more than it gives). Otherwise shares of at most ceil(tiles of all units / aim) tiles, and
+// of one tile for each wave at least.
 struct Plan {
-    int units_per_seq, units, slots, grid;
+    int units_per_seq, units, aim, grid;
     bool whole_units;
 };
-__device__ __forceinline__ int tiles_per_group(const Plan &p, int total) {
-    const int per = (total + p.slots - 1) / p.slots, avg = (total + p.units - 1) / p.units;
-    return max(per, min(avg, kWaves));
+
+// The shares of one unit of sequence `seq`, which is group `first` of the launch plus `units before
+// it in the sequence` times `shares`.
+struct Shares {
+    int seq, n_tiles, shares, first;
+};
+
+__device__ __forceinline__ int shares_of(int n_tiles, int per) {
+    return (n_tiles + per - 1) / per;
+}
+__device__ __forceinline__ int most_tiles(const Plan &p, int all_tiles) {
+    return max((all_tiles * p.units_per_seq + p.aim - 1) / p.aim, kWaves);
 }
 
-__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
-
-// Tiles of all sequences, and of those before sequence `upto`. Every lane of a wave takes part.
-// (The entry point bounds the tiles of all units by 2^31.)
-__device__ __forceinline__ void count_tiles(const AttnArgs &a, const KvView &c, int upto,
-                                            int *total, int *before) {
+// The sequence for which stop(groups before it, groups of it, sequence) holds: every lane of a wave
+// takes part, a lane per sequence. seq = n_seqs if there is none. (The entry point bounds the tiles
+// of all units by 2^31.)
+template <typename Stop>
+__device__ __forceinline__ Shares find_shares(const AttnArgs &a, const KvView &c, const Plan &p,
+                                              Stop stop) {
     const int lane = threadIdx.x & (kWave - 1);
-    int sum = 0, pre = 0;
-    for (int b = lane; b < c.n_seqs; b += kWave) {
-        const int n = visible_keys(a, c, b).n_tiles;
-        sum += n;
-        pre += b < upto ? n : 0;
-    }
-    *total = wave_sum_dpp(sum);
-    *before = wave_sum_dpp(pre);
-}
-
-// The sequence that holds tile `at` of the line, and the tiles of the line before it.
-__device__ __forceinline__ int find_sequence(const AttnArgs &a, const KvView &c, int at,
-                                             int units_per_seq, int *before) {
-    const int lane = threadIdx.x & (kWave - 1);
-    int base = 0;
-    for (int b0 = 0; b0 < c.n_seqs; b0 += kWave) {
-        const int mine = b0 + lane < c.n_seqs
-                             ? visible_keys(a, c, b0 + lane).n_tiles * units_per_seq
-                             : 0;
-        int sum = mine;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const int v = __shfl_up(sum, o, kWave);
-            if (lane >= o) sum += v;
-        }
-        const uint64_t hit = __ballot(base + sum > at);
+    int n = lane < c.n_seqs ? visible_keys(a, c, lane).n_tiles : 0;
+    int all = n;
+    for (int b = lane + kWave; b < c.n_seqs; b += kWave) all += visible_keys(a, c, b).n_tiles;
+    const int per = most_tiles(p, wave_sum_dpp(all));
+    Shares s;
+    for (int b0 = 0, base = 0;;) {
+        const int mine = shares_of(n, per) * p.units_per_seq;
+        const int sum = wave_scan_dpp(mine);
+        const uint64_t hit = __ballot(stop(base + sum - mine, mine, b0 + lane));
         if (hit) {
             const int w = __builtin_ctzll(hit);
-            *before = uniform(base + __shfl(sum - mine, w, kWave));
-            return uniform(b0 + w);
+            s.seq = b0 + w;
+            s.n_tiles = __builtin_amdgcn_readlane(n, w);
+            s.shares = shares_of(s.n_tiles, per);
+            s.first = base + __builtin_amdgcn_readlane(sum - mine, w);
+            return s;
         }
-        base = uniform(base + __shfl(sum, kWave - 1, kWave));
+        base += __builtin_amdgcn_readlane(sum, kWave - 1);
+        b0 += kWave;
+        if (b0 >= c.n_seqs) break;
+        n = b0 + lane < c.n_seqs ? visible_keys(a, c, b0 + lane).n_tiles : 0;
     }
-    *before = base;
-    return c.n_seqs;
+    s.seq = c.n_seqs;
+    s.n_tiles = s.shares = s.first = 0;
+    return s;
 }
 
-// A partial result: `rows` maxima (log2 units), `rows` sums of weights, then rows x D weighted
-// sums. A workgroup has two: of the unit it begins in the middle of (or that outlasts it), and of
-// the last unit it begins.
-__device__ __forceinline__ float *partial(void *work, int64_t group, int which, int rows, int D) {
-    return static_cast<float *>(work) + (2 * group + which) * rows * (D + 2);
+// A share's partial result: `rows` maxima (log2 units), `rows` sums of weights, then rows x D
+// weighted sums.
+__device__ __forceinline__ float *partial(void *work, int64_t group, int rows, int D) {
+    return static_cast<float *>(work) + group * rows * (D + 2);
 }
 
 // The rows of a sequence without keys: zeros.
@@ -126,27 +126,12 @@ __device__ __forceinline__ void write_empty(const AttnArgs &a, const KvView &c, 
 }
 
 // PAGE16: pages of 16 slots and more, so that 16 aligned keys lie in one page.
-#ifndef WPE128
-#define WPE128 3
-#endif
-#ifndef WPE256
-#define WPE256 1
-#endif
-#ifndef WHOLE
-#define WHOLE 8
-#endif
-#ifndef SL64
-#define SL64 4
-#endif
-#ifndef SL128
-#define SL128 3
-#endif
-#ifndef SL256
-#define SL256 2
-#endif
+// Registers: sums, queries and a tile of keys and values take 112 of them at 128 dims (3 waves a
+// SIMD; 4 spill: decode of 4 x 131072 keys 292 us for 188) and 224 at 256 dims (one wave a SIMD; 2
+// spill: 32 x 8192 keys, window 1024, 54 us for 34).
 template <int DP, bool PAGE16>
 __global__ void __launch_bounds__(kWaves * 64)
-__attribute__((amdgpu_waves_per_eu(DP > 128 ? WPE256 : DP > 64 ? WPE128 : 4))) attn_decode_kernel(
+__attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode_kernel(
     AttnArgs a, KvView c, Plan plan) {
     constexpr int KS = DP / 32;      // steps of the first product
     constexpr int DT = DP / 16;      // tiles of the second
@@ -164,50 +149,41 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? WPE256 : DP > 64 ? WPE128 : 4))) a
     const float cs = a.scale * kLog2e;
     uint16_t *my_v = sv[wid];
 
-    // this workgroup's tiles of the line: line0 .. line1
-    int line0, line1, seq_begin, b;
-    if (plan.whole_units) {
-        b = blockIdx.x / plan.units_per_seq;
-        const int n = visible_keys(a, c, b).n_tiles;
-        seq_begin = 0;
-        line0 = static_cast<int>(blockIdx.x % plan.units_per_seq) * n;
-        line1 = line0 + n;
-    } else {
-        int total, unused;
-        count_tiles(a, c, 0, &total, &unused);
-        total *= plan.units_per_seq;
-        const int per = tiles_per_group(plan, total);
-        line0 = static_cast<int>(min(static_cast<int64_t>(blockIdx.x) * per,
-                                     static_cast<int64_t>(total)));
-        line1 = min(line0 + per, total);
-        b = find_sequence(a, c, line0, plan.units_per_seq, &seq_begin);
-    }
-    // A sequence without keys has no tile: its rows are written by the group of its number.
+    // A sequence without keys has no share: its rows are written by the group of its number.
     for (int e = blockIdx.x; e < c.n_seqs; e += gridDim.x)
         if (kv_length(c, e) == 0) write_empty(a, c, e);
 
-    for (int at = line0; at < line1;) {
-        // (an opaque copy: addresses made from it are computed here for each unit, rather than kept
-        // in registers through all of them)
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        const int lane = tid & 63;
+    // this workgroup's share: tiles t0 .. t1 of a unit
+    int b, unit, t0, t1;
+    bool whole;
+    if (plan.whole_units) {
+        b = blockIdx.x / plan.units_per_seq;
+        unit = blockIdx.x % plan.units_per_seq;
+        t0 = 0;
+        t1 = visible_keys(a, c, b).n_tiles;
+        whole = true;
+    } else {
+        const int group = blockIdx.x;
+        const Shares s = find_shares(a, c, plan, [&](int before, int mine, int) {
+            return before <= group && group < before + mine;
+        });
+        if (s.seq == c.n_seqs) return;
+        b = s.seq;
+        unit = (group - s.first) / s.shares;
+        const int i = group - s.first - unit * s.shares;
+        t0 = static_cast<int>(static_cast<int64_t>(s.n_tiles) * i / s.shares);
+        t1 = static_cast<int>(static_cast<int64_t>(s.n_tiles) * (i + 1) / s.shares);
+        whole = s.shares == 1;
+    }
+    if (t0 == t1) return;
+    b = uniform(b);
+    unit = uniform(unit);
+    t0 = uniform(t0);
+    t1 = uniform(t1);
+    {
+        const int tid = threadIdx.x, lane = tid & 63;
         const int r = lane & 15, g = lane >> 4;  // column (query head), group of 16 lanes
-        b = uniform(b);
         const Keys keys = visible_keys(a, c, b);
-        if (keys.n_tiles == 0) {
-            ++b;
-            continue;
-        }
-        const int unit = uniform((at - seq_begin) / keys.n_tiles);
-        if (unit >= plan.units_per_seq) {  // the sequence is done
-            seq_begin += keys.n_tiles * plan.units_per_seq;
-            ++b;
-            continue;
-        }
-        const int unit_begin = seq_begin + unit * keys.n_tiles;
-        const int t0 = uniform(at - unit_begin);
-        const int t1 = uniform(min(line1 - unit_begin, keys.n_tiles));
         const int rt = unit % row_tiles, hk = unit / row_tiles;
         const int head0 = hk * G + rt * kRows;
         const int n_rows = min(G - rt * kRows, kRows);
@@ -400,10 +376,9 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? WPE256 : DP > 64 ? WPE128 : 4))) a
         for (int d = 0; d < DT; ++d)
             *reinterpret_cast<floatx4_t *>(&my_o[r * kRow + 16 * d + 4 * g]) = o[d];
         __syncthreads();
-        const bool whole = t0 == 0 && t1 == keys.n_tiles;
         const bool wide = wide_rows(a);
         const int slot_rows = min(G, kRows);
-        float *part = partial(a.work, blockIdx.x, at == line0 ? 0 : 1, slot_rows, D);
+        float *part = partial(a.work, blockIdx.x, slot_rows, D);
         for (int e = tid; e < n_rows * (DP / 4); e += kWaves * 64) {
             const int row = e / (DP / 4), d = e % (DP / 4) * 4;
             if (d >= D) continue;
@@ -433,8 +408,6 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? WPE256 : DP > 64 ? WPE128 : 4))) a
                 }
             }
         }
-        at = unit_begin + t1;
-        if (at < line1) __syncthreads();  // before the next unit's values overwrite the sums
     }
 }
 
@@ -447,20 +420,13 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvV
     const int64_t pair = blockIdx.x;
     const int b = static_cast<int>(pair / a.n_heads), head = static_cast<int>(pair % a.n_heads);
     const int G = a.n_heads / c.n_kv, D = c.head_dim, rows = min(G, kRows);
-    const int n_tiles = visible_keys(a, c, b).n_tiles;
-    if (n_tiles == 0) return;
-    int total, before;
-    count_tiles(a, c, b, &total, &before);
-    const int per = tiles_per_group(plan, total * plan.units_per_seq);
+    const Shares s = find_shares(a, c, plan, [&](int, int, int seq) { return seq == b; });
+    if (s.shares <= 1) return;  // written by the first kernel
     const int row_tiles = (G + kRows - 1) / kRows, in_group = head % G;
     const int unit = head / G * row_tiles + in_group / kRows, row = in_group % kRows;
-    const int u0 = before * plan.units_per_seq + unit * n_tiles;
-    const int g0 = u0 / per, g1 = (u0 + n_tiles - 1) / per;
-    if (g0 == g1) return;  // written by the first kernel
-    const int n = g1 - g0 + 1;
-    // the unit is the last that its first group begins, unless it begins with the group
+    const int n = s.shares;
     const auto part = [&](int i) {
-        return partial(a.work, g0 + i, i == 0 && u0 % per != 0 ? 1 : 0, rows, D);
+        return partial(a.work, s.first + unit * n + i, rows, D);
     };
     const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
 
@@ -509,13 +475,21 @@ Plan plan_of(int n_heads, const KvView &c, int window, int sinks) {
     if (window > 0 && int64_t(window) + sinks + 4 * kTile < keys)
         keys = int64_t(window) + sinks + 4 * kTile;
     const int64_t tiles = (keys + kTile - 1) / kTile;
-    p.whole_units = tiles <= WHOLE;
-    p.slots = device_cu_count() * (c.head_dim > 128 ? SL256 : c.head_dim > 64 ? SL128 : SL64);
-    // no more groups than tiles_per_group can make of the most tiles there can be
-    const int64_t most = (tiles * p.units + kWaves - 1) / kWaves;
-    int64_t grid = p.slots < most ? p.slots : most;
-    if (p.whole_units || grid < p.units) grid = p.units;
-    p.grid = static_cast<int>(grid);
+    const int cus = device_cu_count();
+    // One launch instead of two, the longest unit's pass instead of a share's. Measured at 28 / 4
+    // heads of 128, us whole / cut: one sequence of 500 keys 10.1 / 10.4, of 1000 16.0 / 10.4; 64
+    // sequences (a unit for every compute unit) of 1000 keys 28 / 35, of 2000 50 / 58.
+    p.whole_units = tiles <= (p.units >= cus ? 64 : 16);
+    // Workgroups that run at once (by registers; 6 at 64 dims measured better than the 4 that fit:
+    // 64 x 3000 keys, 8 heads, 76 us for 85). Few units: shares that fill the card once, where every
+    // unit rounds up by half a share. Many: about two rounds, which even out by themselves. (32 ragged
+    // sequences of up to 8192 keys, 128 units, us at 1 / 2 / 3 / 4 times the compute units: 78 / 73 /
+    // 65 / 64; 100 of up to 6000, 400 units: 164 / 144 / 144 / 144, at 6 times 141.)
+    const int resident = cus * (c.head_dim > 128 ? 1 : c.head_dim > 64 ? 3 : 6);
+    p.aim = p.units <= resident / 2 ? resident - p.units / 2 : 2 * resident;
+    const int64_t most = p.units * ((tiles + kWaves - 1) / kWaves);  // shares of kWaves tiles
+    const int64_t grid = static_cast<int64_t>(p.units) + p.aim;
+    p.grid = p.whole_units ? p.units : static_cast<int>(grid < most ? grid : most);
     return p;
 }
 
@@ -541,7 +515,7 @@ size_t attn_decode_work_bytes(int n_heads, const KvView &c, int window, int sink
     const Plan p = plan_of(n_heads, c, window, sinks);
     const int G = n_heads / c.n_kv;
     if (p.whole_units) return 0;
-    return sizeof(float) * 2 * p.grid * (G < kRows ? G : kRows) * (c.head_dim + 2);
+    return sizeof(float) * p.grid * (G < kRows ? G : kRows) * (c.head_dim + 2);
 }
 
 hipError_t launch_attn_decode(const AttnArgs &a, const KvView &c, hipStream_t stream) {

@@ -62,6 +62,19 @@ __device__ __forceinline__ bool wide_rows(const AttnArgs &a) {
     return (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 }
 
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Sum over lanes 0 .. own lane (row shifts, then the rows' totals to the rows after them).
+__device__ __forceinline__ int wave_scan_dpp(int v) {
+    v += dpp_i<0x111, 0xF, true>(v);
+    v += dpp_i<0x112, 0xF, true>(v);
+    v += dpp_i<0x114, 0xF, true>(v);
+    v += dpp_i<0x118, 0xF, true>(v);
+    v += dpp_i<0x142, 0xA, false>(v);
+    v += dpp_i<0x143, 0xC, false>(v);
+    return v;
+}
+
 __device__ __forceinline__ float other_half(float v) {  // the value of lane ^ 32
     return __shfl_xor(v, 32, kWave);
 }

@@ -45,25 +45,21 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
         }
         const int nq = max(end - begin, 0);
         const int mine = static_cast<int>((static_cast<int64_t>(nq) * G + BM - 1) / BM);
-        int sum = mine;
-#pragma unroll
-        for (int o = 1; o < kWave; o <<= 1) {
-            const int v = __shfl_up(sum, o, kWave);
-            if (lane >= o) sum += v;
-        }
+        const int sum = wave_scan_dpp(mine);
         const uint64_t hit = __ballot(before + sum > tile);
         if (hit) {
             const int w = __builtin_ctzll(hit);
-            const int left = tile - before - (__shfl(sum, w, kWave) - __shfl(mine, w, kWave));
-            const int n_rows = __shfl(nq, w, kWave) * G;
+            const int tokens = __builtin_amdgcn_readlane(nq, w);
+            const int tiles = __builtin_amdgcn_readlane(mine, w);
+            const int left = tile - before - (__builtin_amdgcn_readlane(sum, w) - tiles);
             out->seq = base + w;
-            out->rows = n_rows;
-            out->row0 = (__shfl(mine, w, kWave) - 1 - left) * BM;
-            out->q0 = __shfl(begin, w, kWave);
-            out->pos0 = kv_length(c, base + w) - __shfl(nq, w, kWave);
+            out->rows = tokens * G;
+            out->row0 = (tiles - 1 - left) * BM;
+            out->q0 = __builtin_amdgcn_readlane(begin, w);
+            out->pos0 = kv_length(c, base + w) - tokens;
             return true;
         }
-        before += __shfl(sum, kWave - 1, kWave);
+        before += __builtin_amdgcn_readlane(sum, kWave - 1);
     }
     return false;
 }
