@@ -201,7 +201,9 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
 
         const int32_t *table = c.table + b * c.ld_table;
         const int64_t head_off = static_cast<int64_t>(hk) * c.head_stride;
-        const auto visible = [&](int p) { return p <= keys.last && (p >= keys.lo || p < a.sinks); };
+        const auto visible = [&](int p) {
+            return (p <= keys.last) & ((p >= keys.lo) | (p < a.sinks));
+        };
         // 16 keys as they are read: the page offset of a visible key among them (of the newest key if
         // there is none), and that key. Keys that are not visible are read from it: finite values,
         // whose weight is 0.
@@ -416,7 +418,7 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
 constexpr int kJoinThreads = 256;
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvView c, Plan plan) {
     __shared__ floatx4_t so[kJoinThreads];
-    __shared__ float red[kJoinThreads / 64], sw[kJoinThreads];
+    __shared__ float sm[kJoinThreads], sl[kJoinThreads];
     const int64_t pair = blockIdx.x;
     const int b = static_cast<int>(pair / a.n_heads), head = static_cast<int>(pair % a.n_heads);
     const int G = a.n_heads / c.n_kv, D = c.head_dim, rows = min(G, kRows);
@@ -428,38 +430,34 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvV
     const auto part = [&](int i) {
         return partial(a.work, s.first + unit * n + i, rows, D);
     };
-    const int tid = threadIdx.x, lane = tid & 63, wid = tid >> 6;
-
-    float m = kNoMax;
-    for (int i = tid; i < n; i += kJoinThreads) m = fmaxf(m, part(i)[row]);
-    m = wave_max(m);
-    if (lane == 0) red[wid] = m;
-    __syncthreads();
-    m = red[0];
-#pragma unroll
-    for (int w = 1; w < kJoinThreads / 64; ++w) m = fmaxf(m, red[w]);
-
+    const int tid = threadIdx.x;
     const int lanes = D / 4;                  // threads over the dims, 4 each
     const int groups = kJoinThreads / lanes;  // (threads past groups * lanes idle)
     const int grp = tid / lanes, d = tid % lanes * 4;
-    float l = 0.0f;
+    float m = kNoMax, l = 0.0f;
     floatx4_t v = floatx4_t(0.0f);
+    const auto add = [&](float m1, float l1, floatx4_t v1) {
+        const float m2 = fmaxf(m, m1);
+        const float f = __builtin_amdgcn_exp2f(m - m2), f1 = __builtin_amdgcn_exp2f(m1 - m2);
+        m = m2;
+        l = l * f + l1 * f1;
+        v = v * f + v1 * f1;
+    };
     if (grp < groups) {
+#pragma unroll 4
         for (int i = grp; i < n; i += groups) {
             const float *p = part(i);
-            const float f = __builtin_amdgcn_exp2f(p[row] - m);
-            l += f * p[rows + row];
-            v += f * *reinterpret_cast<const floatx4_t *>(p + 2 * rows + row * D + d);
+            add(p[row], p[rows + row],
+                *reinterpret_cast<const floatx4_t *>(p + 2 * rows + row * D + d));
         }
         so[tid] = v;
-        sw[tid] = l;
+        sm[tid] = m;
+        sl[tid] = l;
     }
     __syncthreads();
     if (tid >= lanes) return;
-    for (int q = 1; q < groups; ++q) {
-        v += so[q * lanes + tid];
-        l += sw[q * lanes + tid];
-    }
+    for (int q = 1; q < groups; ++q)
+        add(sm[q * lanes + tid], sl[q * lanes + tid], so[q * lanes + tid]);
     v *= l > 0.0f ? 1.0f / l : 0.0f;
     store_out4(a.y, b * a.ldy + static_cast<int64_t>(head) * D + d, v, a.out_f32, wide_rows(a));
     if (a.lse && d == 0) a.lse[pair] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;

@@ -76,7 +76,9 @@ __device__ __forceinline__ int wave_scan_dpp(int v) {
 }
 
 __device__ __forceinline__ float other_half(float v) {  // the value of lane ^ 32
-    return __shfl_xor(v, 32, kWave);
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
 }
 
 }  // namespace w4

@@ -102,6 +102,7 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     // Key tiles: those of the sinks, then those from the oldest key in a row's window on.
     const int lo = a.window > 0 ? max(tile_first - a.window + 1, 0) : 0;
     const int n_sink = a.window > 0 ? (min(a.sinks, max(lo, 0)) + KT - 1) / KT : 0;
+    const int sinks_end = a.window > 0 ? a.sinks : 0;  // (lo is 0 without a window)
     const int lo_tile = max(lo / KT, n_sink);
     const int n_iter = tile_last < 0 ? 0 : n_sink + tile_last / KT + 1 - lo_tile;
 
@@ -120,34 +121,38 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     floatx16_t o[DT];
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = floatx16_t(0.0f);
-    const float cs = a.scale * kLog2e;
+    // (a scale of 0 as one that moves no weight, so that hidden scores of -inf stay -inf)
+    const float cs = fmaxf(a.scale * kLog2e, 1e-37f);
+    const int before = a.window > 0 ? pos - a.window : -1;  // newest position out of the window
     float M = kNoMax, l = 0.0f;
 
     // Staging: this thread's chunk of rows r0, r0 + kRowStep, ... of each tile. A row whose key no
-    // row of the block sees is read from one that some row sees (finite; its weights are 0).
+    // row of the block sees is read from one that some row sees (finite; its weights are 0), dims
+    // past D from the row's last chunk (they meet zeros of q, or outputs that are not kept). The
+    // page table entries are read a tile ahead of the rows, the rows a tile ahead of their use.
     const int my_chunk = tid % kChunks, r0 = tid / kChunks;
-    const bool my_dims = my_chunk * 8 < D;
+    const int my_col = hk * c.head_stride + min(8 * my_chunk, D - 8);
     const int32_t *table = c.table + t.seq * c.ld_table;
     const auto tile_key = [&](int it) { return (it < n_sink ? it : lo_tile + it - n_sink) * KT; };
-    int64_t at[kLoads];
-    const auto locate = [&](int it) {
-        const int k0 = tile_key(it);
+    const auto key_of = [&](int it, int i) {
+        const int p = min(tile_key(it) + r0 + i * kRowStep, tile_last);
+        return p >= sinks_end && p < lo ? lo : p;
+    };
+    int entry[kLoads];
+    const auto look_up = [&](int it) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            int p = min(k0 + r0 + i * kRowStep, tile_last);
-            if (a.window > 0 && p >= a.sinks && p < lo) p = lo;
-            at[i] = kv_offset(c, table, p, hk) + my_chunk * 8;
-        }
+        for (int i = 0; i < kLoads; ++i)
+            entry[i] = read_const(table + (key_of(it, i) >> c.page_shift));
     };
     uintx4_t rk[kLoads], rv[kLoads];
-    const auto fetch = [&] {
+    const auto fetch = [&](int it) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
-            rk[i] = rv[i] = uintx4_t{0, 0, 0, 0};
-            if (my_dims) {
-                rk[i] = *reinterpret_cast<const uintx4_t *>(c.k + at[i]);
-                rv[i] = *reinterpret_cast<const uintx4_t *>(c.v + at[i]);
-            }
+            const int page = min(max(entry[i], 0), c.n_pages - 1);
+            const int64_t at = static_cast<int64_t>(page) * c.page_stride +
+                               ((key_of(it, i) & c.page_mask) * c.slot_stride + my_col);
+            rk[i] = *reinterpret_cast<const uintx4_t *>(c.k + at);
+            rv[i] = *reinterpret_cast<const uintx4_t *>(c.v + at);
         }
     };
     const auto stage = [&](int buf) {
@@ -159,18 +164,20 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
         }
     };
     if (n_iter > 0) {
-        locate(0);
-        fetch();
-        if (n_iter > 1) locate(1);
+        look_up(0);
+        fetch(0);
+        look_up(min(1, n_iter - 1));
         stage(0);
     }
     __syncthreads();
 
-    for (int it = 0; it < n_iter; ++it) {
+    if (n_iter > 0) {
+    int it = 0;
+    do {
         const int buf = it & 1;
         if (it + 1 < n_iter) {
-            fetch();
-            if (it + 2 < n_iter) locate(it + 2);
+            fetch(it + 1);
+            look_up(min(it + 2, n_iter - 1));
         }
         const int k0 = tile_key(it);
         // any key of the tile that some row of the wave sees?
@@ -192,20 +199,15 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
             const bool whole =
                 k0 + KT - 1 <= first &&
                 (a.window == 0 || k0 > last - a.window || k0 + KT - 1 < a.sinks);
-            uint32_t vis[SUB];
             if (!whole) {
 #pragma unroll
-                for (int u = 0; u < SUB; ++u) {
-                    vis[u] = 0;
+                for (int u = 0; u < SUB; ++u)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         const int j = k0 + 32 * u + 8 * (i / 4) + 4 * half + i % 4;
-                        const bool ok = j <= pos && (a.window == 0 || j > pos - a.window ||
-                                                     j < a.sinks);
-                        vis[u] |= ok ? 1u << i : 0u;
+                        const bool ok = (j <= pos) & ((j > before) | (j < a.sinks));
                         s[u][i] = ok ? s[u][i] : -INFINITY;
                     }
-                }
             }
             float mx = s[0][0];
 #pragma unroll
@@ -227,12 +229,8 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
                 uintx4_t w[2];
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
-                    float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], cs, -M));
-                    float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], cs, -M));
-                    if (!whole) {
-                        p0 = (vis[u] >> i) & 1 ? p0 : 0.0f;
-                        p1 = (vis[u] >> (i + 1)) & 1 ? p1 : 0.0f;
-                    }
+                    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], cs, -M));
+                    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], cs, -M));
                     l += p0 + p1;
                     w[i / 8][i % 8 / 2] = pack_bf16(p0, p1);
                 }
@@ -260,6 +258,7 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
         }
         if (it + 1 < n_iter) stage(buf ^ 1);
         __syncthreads();
+    } while (++it < n_iter);
     }
 
     l += other_half(l);
