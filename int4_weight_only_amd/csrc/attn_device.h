@@ -75,10 +75,26 @@ __device__ __forceinline__ int wave_scan_dpp(int v) {
     return v;
 }
 
+// Largest of 64 values >= 0.
+__device__ __forceinline__ int wave_max_dpp(int v) {
+    v = max(v, dpp_i<0x111, 0xF, true>(v));
+    v = max(v, dpp_i<0x112, 0xF, true>(v));
+    v = max(v, dpp_i<0x114, 0xF, true>(v));
+    v = max(v, dpp_i<0x118, 0xF, true>(v));
+    v = max(v, dpp_i<0x142, 0xA, false>(v));
+    v = max(v, dpp_i<0x143, 0xC, false>(v));
+    return __builtin_amdgcn_readlane(v, 63);
+}
+
 __device__ __forceinline__ float other_half(float v) {  // the value of lane ^ 32
     const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
                                                     false);
     return __uint_as_float(threadIdx.x & 32 ? r[0] : r[1]);
+}
+__device__ __forceinline__ float max_of_halves(float v) {  // over lane and lane ^ 32
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 }  // namespace w4

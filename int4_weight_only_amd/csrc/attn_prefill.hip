@@ -23,14 +23,20 @@ namespace w4 {
 namespace {
 
 constexpr int kSlack = 8;
+#ifndef AH256
+#define AH256 2
+#endif
 
-struct Tile {  // the rows of a block
-    int seq, row0, rows;      // rows of the sequence's G * nq stacked rows; rows = those in all
-    int q0, pos0;             // token row of stacked row 0, its position
+// A block's rows: of sequence `seq`, stacked rows row0 .. row0 + BM - 1 of `rows`; token row q0 and
+// position pos0 of stacked row 0.
+struct Tile {
+    int seq, row0, rows, q0, pos0;
 };
 
-// The tile'th tile of BM rows, counted through the sequences in order, the last rows of a sequence
-// (which see the most keys) first. Every lane of every wave takes part.
+// Tiles of BM rows of all sequences in the order in which they are given out: the tiles that see
+// most keys first (by their level: the tile's number in its sequence plus the tiles its earlier keys
+// would make), so that the last ones to run are short. Up to 64 sequences, a lane each; more are
+// taken in order, the last rows of each first. Every lane of every wave takes part.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_start, int64_t T,
                                           int G, int tile, Tile *out) {
@@ -38,52 +44,119 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
     int before = 0;
     for (int base = 0; base < c.n_seqs; base += kWave) {
         const int b = base + lane;
-        int begin = 0, end = 0;
+        int begin = 0, nq = 0, n_keys = 0;
         if (b < c.n_seqs) {
             begin = max(read_const(q_start + b), 0);
-            end = min(read_const(q_start + b + 1), static_cast<int>(T));
+            nq = max(min(read_const(q_start + b + 1), static_cast<int>(T)) - begin, 0);
+            n_keys = kv_length(c, b);
         }
-        const int nq = max(end - begin, 0);
-        const int mine = static_cast<int>((static_cast<int64_t>(nq) * G + BM - 1) / BM);
+        const int mine = (nq * G + BM - 1) / BM;
         const int sum = wave_scan_dpp(mine);
-        const uint64_t hit = __ballot(before + sum > tile);
-        if (hit) {
-            const int w = __builtin_ctzll(hit);
-            const int tokens = __builtin_amdgcn_readlane(nq, w);
-            const int tiles = __builtin_amdgcn_readlane(mine, w);
-            const int left = tile - before - (__builtin_amdgcn_readlane(sum, w) - tiles);
-            out->seq = base + w;
-            out->rows = tokens * G;
-            out->row0 = (tiles - 1 - left) * BM;
-            out->q0 = __builtin_amdgcn_readlane(begin, w);
-            out->pos0 = kv_length(c, base + w) - tokens;
-            return true;
+        const int all = __builtin_amdgcn_readlane(sum, kWave - 1);
+        if (tile >= before + all) {
+            before += all;
+            continue;
         }
-        before += __builtin_amdgcn_readlane(sum, kWave - 1);
+        int w, row_tile;  // the lane of the sequence, the tile's number in it
+        if (c.n_seqs <= kWave) {
+            // levels first .. first + mine - 1 are this sequence's; the largest level with more than
+            // `tile` tiles at it or above
+            const int first = static_cast<int>(
+                min(static_cast<int64_t>(max(n_keys - nq, 0)) * G / BM, int64_t{1} << 29));
+            int lo = 0, hi = wave_max_dpp(first + mine);
+            while (lo < hi) {
+                const int mid = lo + (hi - lo + 1) / 2;
+                const int above = max(min(first + mine - mid, mine), 0);
+                if (wave_sum_dpp(above) > tile)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            const int above = wave_sum_dpp(max(min(first + mine - (lo + 1), mine), 0));
+            const int here = (first <= lo) & (lo < first + mine);
+            const int rank = wave_scan_dpp(here);  // (with every lane: outside of any condition)
+            const uint64_t hit = __ballot((here != 0) & (rank == tile - above + 1));
+            if (!hit) return false;
+            w = __builtin_ctzll(hit);
+            row_tile = lo - __builtin_amdgcn_readlane(first, w);
+        } else {
+            const uint64_t hit = __ballot(before + sum > tile);
+            if (!hit) return false;
+            w = __builtin_ctzll(hit);
+            row_tile = before + __builtin_amdgcn_readlane(sum, w) - tile - 1;
+        }
+        const int tokens = __builtin_amdgcn_readlane(nq, w);
+        out->seq = base + w;
+        out->rows = tokens * G;
+        out->row0 = row_tile * BM;
+        out->q0 = __builtin_amdgcn_readlane(begin, w);
+        out->pos0 = __builtin_amdgcn_readlane(n_keys, w) - tokens;
+        return true;
     }
     return false;
 }
 
-template <int DP, int NW, int KT>
+// Orders a multiplying phase: NV products with value fragments (two LDS reads each), then NK with
+// key fragments (one each), every read AHEAD products before its use. (Left to itself the scheduler
+// keeps two fragments in flight, and a product waits for most of an LDS read.)
+template <int NV, int NK, int AHEAD>
+__device__ __forceinline__ void order_phase() {
+    constexpr int kMfma = 0x008, kLdsRead = 0x100;
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, 2 * AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < NV + NK; ++i) {
+        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+        if (i + AHEAD < NV)
+            __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
+        else if (i + AHEAD < NV + NK)
+            __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+    }
+}
+
+// Barrier between phases, after this wave's LDS accesses; loads from memory stay in flight.
+__device__ __forceinline__ void phase_barrier() {
+    phase_fence();
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); vmcnt and expcnt not waited for
+    __builtin_amdgcn_s_barrier();
+    phase_fence();
+}
+
+// Partial results of split `part`: per (token row, head) D weighted sums, and the pair (maximum in
+// log2 units, sum of weights).
+struct Partials {
+    float *o, *ml;
+};
+__device__ __forceinline__ Partials partials(void *work, int64_t pairs, int splits, int part,
+                                             int D) {
+    float *base = static_cast<float *>(work);
+    return {base + part * pairs * D, base + splits * pairs * D + part * pairs * 2};
+}
+
+// What lies in one page: a tile (pages of KT slots and more), the rows a wave stages in one
+// instruction (8 at most, aligned: pages of 8 slots and more), or a row.
+enum { kAnyPages = 0, kSpanPages = 1, kTilePages = 2 };
+
+template <int DP, int NW, int KT, int PAGES>
 __global__ void __launch_bounds__(NW * 64)
-__attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c, int n_tiles) {
+__attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c, int splits) {
     constexpr int BM = NW * 32;
-    constexpr int kChunks = DP / 8;
-    constexpr int kThreads = NW * 64;
-    constexpr int kLoads = KT * kChunks / kThreads;  // 16-byte chunks a thread stages of K, of V
-    static_assert(KT * kChunks % kThreads == 0, "every thread stages the same number of chunks");
-    constexpr int kRowStep = kThreads / kChunks;  // rows between a thread's chunks
+    constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
+    constexpr int kSpan = 64 / kChunks;                // rows a wave stages in one instruction
+    constexpr int kLoads = KT / (NW * kSpan);          // instructions a wave stages a tile with
+    static_assert(kLoads * NW * kSpan == KT, "every wave stages the same number of rows");
+    constexpr int kDepth = DP > 128 || (DP > 64 && NW == 4) ? 1 : 2;           // tiles in flight (registers decide)
     constexpr int kKeyRow = Rows<DP>::kKey, kValueRow = Rows<DP>::kValue;
     constexpr int DT = DP / 32, KS = DP / 16, SUB = KT / 32;
+    constexpr int kGroups = NW / 4;
     __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * kKeyRow];
     __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * kValueRow];
 
-    const int tid = threadIdx.x, lane = tid & 63;
-    const int wid = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int hk = blockIdx.x % c.n_kv;
+    const int lane = threadIdx.x & 63;
+    const int wid = uniform(threadIdx.x >> 6);
     const int G = a.n_heads / c.n_kv, D = c.head_dim;
+    const int hk = blockIdx.x % c.n_kv, part = blockIdx.x / c.n_kv % splits;
     Tile t;
-    if (!find_tile<BM>(c, a.q_start, a.T, G, blockIdx.x / c.n_kv, &t)) return;
+    if (!find_tile<BM>(c, a.q_start, a.T, G, blockIdx.x / c.n_kv / splits, &t)) return;
 
     const int half = lane >> 5;
     const int row = t.row0 + wid * 32 + (lane & 31);
@@ -92,19 +165,25 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     const int head = hk * G + (safe_row - tok * G);
     const int pos = t.pos0 + tok;
 
-    // the wave's rows: positions first .. last; the block's: tile_first .. tile_last
+    // positions of the block's rows (tile_first .. tile_last) and of the wave's (first .. last)
     const int tile_first = t.pos0 + t.row0 / G;
     const int tile_last = t.pos0 + min(t.row0 + BM - 1, t.rows - 1) / G;
-    const int wave_row = min(t.row0 + wid * 32, t.rows - 1);
-    const int first = t.pos0 + wave_row / G;
+    const int first = t.pos0 + min(t.row0 + wid * 32, t.rows - 1) / G;
     const int last = t.pos0 + min(t.row0 + wid * 32 + 31, t.rows - 1) / G;
 
-    // Key tiles: those of the sinks, then those from the oldest key in a row's window on.
+    // Key tiles: those of the sinks, then those from the oldest key in a row's window on; of them
+    // this split's.
     const int lo = a.window > 0 ? max(tile_first - a.window + 1, 0) : 0;
-    const int n_sink = a.window > 0 ? (min(a.sinks, max(lo, 0)) + KT - 1) / KT : 0;
-    const int sinks_end = a.window > 0 ? a.sinks : 0;  // (lo is 0 without a window)
+    const int sinks_end = a.window > 0 ? a.sinks : 0;
+    const int n_sink = (min(sinks_end, lo) + KT - 1) / KT;
     const int lo_tile = max(lo / KT, n_sink);
-    const int n_iter = tile_last < 0 ? 0 : n_sink + tile_last / KT + 1 - lo_tile;
+    const int n_all = tile_last < 0 ? 0 : n_sink + tile_last / KT + 1 - lo_tile;
+    const int it0 = static_cast<int>(static_cast<int64_t>(n_all) * part / splits);
+    const int n_iter = static_cast<int>(static_cast<int64_t>(n_all) * (part + 1) / splits) - it0;
+    const auto tile_key = [&](int it) {
+        it += it0;
+        return (it < n_sink ? it : lo_tile + it - n_sink) * KT;
+    };
 
     // Q^T: lane holds dims 16 s + 8 half .. + 7 of its row
     bf16x8_t qf[KS];
@@ -126,147 +205,280 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     const int before = a.window > 0 ? pos - a.window : -1;  // newest position out of the window
     float M = kNoMax, l = 0.0f;
 
-    // Staging: this thread's chunk of rows r0, r0 + kRowStep, ... of each tile. A row whose key no
-    // row of the block sees is read from one that some row sees (finite; its weights are 0), dims
-    // past D from the row's last chunk (they meet zeros of q, or outputs that are not kept). The
-    // page table entries are read a tile ahead of the rows, the rows a tile ahead of their use.
-    const int my_chunk = tid % kChunks, r0 = tid / kChunks;
-    const int my_col = hk * c.head_stride + min(8 * my_chunk, D - 8);
+    // Staging: in each of kLoads instructions a wave moves kSpan consecutive rows of the tile. A row
+    // whose key no row of the block sees is read from one that some row sees (finite; its weights are
+    // 0; of the same rows, if there is any); dims past D from the row's last chunk (they meet zeros of
+    // q, or outputs that are not kept).
+    const int my_row = lane / kChunks, my_col = min(8 * (lane % kChunks), D - 8);
     const int32_t *table = c.table + t.seq * c.ld_table;
-    const auto tile_key = [&](int it) { return (it < n_sink ? it : lo_tile + it - n_sink) * KT; };
-    const auto key_of = [&](int it, int i) {
-        const int p = min(tile_key(it) + r0 + i * kRowStep, tile_last);
-        return p >= sinks_end && p < lo ? lo : p;
+    const uint16_t *head_k = c.k + static_cast<int64_t>(hk) * c.head_stride;
+    const uint16_t *head_v = c.v + static_cast<int64_t>(hk) * c.head_stride;
+    const auto span_at = [&](int i) { return (i * NW + wid) * kSpan; };
+    const auto all_seen = [&](int k0) {  // each key of the tile by some row of the block
+        return (k0 + KT - 1 <= tile_last) & ((k0 >= lo) | (k0 + KT - 1 < sinks_end));
     };
-    int entry[kLoads];
-    const auto look_up = [&](int it) {
+    const auto visible = [&](int p) {
+        return (p <= tile_last) & ((p >= lo) | (p < sinks_end));
+    };
+    const auto safe_of = [&](int s0, int n) {  // a key that is seen, among the n from s0 on if any is
+        if (s0 > tile_last) return tile_last;
+        if (s0 < sinks_end) return s0;
+        return s0 + n - 1 < lo ? lo : max(s0, lo);
+    };
+    const auto page_offset = [&](int page) {
+        return static_cast<int64_t>(min(max(page, 0), c.n_pages - 1)) * c.page_stride;
+    };
+    // A tile's rows for this lane: a base (uniform but for PAGES == kAnyPages) and an offset.
+    constexpr int kBases = PAGES == kTilePages ? 1 : kLoads;
+    struct Where {
+        int64_t base[kBases];
+        uint32_t off[kLoads];
+    };
+    uint32_t seen_off[kLoads];  // the offsets in a tile whose rows are all seen
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+        seen_off[i] = ((PAGES == kTilePages ? span_at(i) : 0) + my_row) * c.slot_stride + my_col;
+    int entry[kBases];
+    const auto look_up = [&](int it) {  // the page table entries of a tile
+        const int k0 = tile_key(it);
+        if constexpr (PAGES == kTilePages) {
+            entry[0] = read_const(table + (k0 >> c.page_shift));  // (its first key or a later one is seen)
+        } else if constexpr (PAGES == kSpanPages) {
+            const bool all = all_seen(k0);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int s0 = k0 + span_at(i);
+                entry[i] = read_const(table + ((all ? s0 : safe_of(s0, kSpan)) >> c.page_shift));
+            }
+        }
+    };
+    const auto locate = [&](int it, Where &w) {
+        const int k0 = tile_key(it);
+        if constexpr (PAGES == kTilePages) {
+            w.base[0] = page_offset(entry[0]) +
+                        static_cast<int64_t>((k0 & c.page_mask) * c.slot_stride);
+            const int safe = k0 < sinks_end ? k0 : max(k0, lo);
+            const uint32_t other = (safe - k0) * c.slot_stride + my_col;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                w.off[i] = visible(k0 + span_at(i) + my_row) ? seen_off[i] : other;
+        } else {
+            const bool all = all_seen(k0);
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int s0 = k0 + span_at(i), p = s0 + my_row;
+                const int safe = all ? s0 : safe_of(s0, kSpan);
+                const bool vis = all | visible(p);
+                if constexpr (PAGES == kSpanPages) {
+                    // the span's first row if the span has a row that is seen, else the row instead
+                    const int first_row = safe >= s0 && safe < s0 + kSpan ? s0 : safe;
+                    w.base[i] = page_offset(entry[i]) +
+                                static_cast<int64_t>((first_row & c.page_mask) * c.slot_stride);
+                    w.off[i] = vis ? seen_off[i] : (safe - first_row) * c.slot_stride + my_col;
+                } else {
+                    const int from = vis ? p : safe;
+                    w.base[i] = page_offset(read_const(table + (from >> c.page_shift)));
+                    w.off[i] = (from & c.page_mask) * c.slot_stride + my_col;
+                }
+            }
+        }
+    };
+    const auto fetch = [&](const uint16_t *kv, const Where &w, uintx4_t *r) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            entry[i] = read_const(table + (key_of(it, i) >> c.page_shift));
+            r[i] = *reinterpret_cast<const uintx4_t *>(
+                reinterpret_cast<const char *>(kv + w.base[PAGES == kTilePages ? 0 : i]) +
+                2u * w.off[i]);
     };
-    uintx4_t rk[kLoads], rv[kLoads];
-    const auto fetch = [&](int it) {
+    const auto put = [&](uint16_t *dst, int stride, const uintx4_t *r) {
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int page = min(max(entry[i], 0), c.n_pages - 1);
-            const int64_t at = static_cast<int64_t>(page) * c.page_stride +
-                               ((key_of(it, i) & c.page_mask) * c.slot_stride + my_col);
-            rk[i] = *reinterpret_cast<const uintx4_t *>(c.k + at);
-            rv[i] = *reinterpret_cast<const uintx4_t *>(c.v + at);
+        for (int i = 0; i < kLoads; ++i)
+            *reinterpret_cast<uintx4_t *>(
+                &dst[(span_at(i) + my_row) * stride + 8 * (lane % kChunks)]) = r[i];
+    };
+    // Rows on their way. Phase A(i) stages the keys of tile i + 2 and the values of tile i + 1, and
+    // sends for the keys of tile i + 2 + kDepth and the values of the tile before that in their place.
+    // (Past the last tile both repeat it, into buffers that nothing reads any more.)
+    struct Set {
+        uintx4_t k[kLoads], v[kLoads];
+    };
+    Where newest;  // of the newest tile whose keys were sent for
+    const auto tile_at = [&](int it) { return min(it, n_iter - 1); };
+    const auto stage = [&](int it, Set &x) __attribute__((always_inline)) {
+        put(sk[it & 1], kKeyRow, x.k);
+        put(sv[(it + 1) & 1], kValueRow, x.v);
+        fetch(head_v, newest, x.v);
+        locate(tile_at(it + 2 + kDepth), newest);
+        fetch(head_k, newest, x.k);
+    };
+
+    // The two products and the softmax of a tile alternate with a barrier between them: phase A
+    // multiplies (the values of tile i, the keys of tile i + 1) and stages, phase B turns the scores
+    // into weights. With two groups of four waves (one of each on every SIMD), the second runs one
+    // phase behind the first, so that one multiplies while the other computes weights.
+    //   phase        0        1        2        3
+    //   group 0      A(-1)    B(-1)    A(0)     B(0)  ...
+    //   group 1               A(-1)    B(-1)    A(0)  ...
+    // A(i) reads keys i + 1 and values i and writes keys i + 2 and values i + 1 into the other buffers:
+    // group 0's A(i) comes after the last phase that reads what was there (group 1's A(i - 1)), group
+    // 1's A(i) before the first that reads the new (group 0's A(i + 1)).
+    const int group = kGroups > 1 ? wid / 4 : 0;
+    floatx16_t s[SUB];
+    bf16x8_t pf[SUB][2];
+
+    const auto scores = [&](int it) __attribute__((always_inline)) {
+        const uint16_t *kp = &sk[it & 1][(lane & 31) * kKeyRow + 8 * half];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) s[u] = floatx16_t(0.0f);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+                s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    *reinterpret_cast<const bf16x8_t *>(kp + 32 * u * kKeyRow + 16 * ks), qf[ks],
+                    s[u], 0, 0, 0);
+    };
+    // O^T += V^T P^T, 16 keys a step: slots 8 half + 0..3 are keys 4 half + 0..3 of the step, slots
+    // 8 half + 4..7 keys 8 + 4 half + 0..3
+    const auto weigh = [&](int it) __attribute__((always_inline)) {
+        const uint16_t *vp = &sv[it & 1][(4 * half + (lane & 15) / 4) * kValueRow + (lane & 16) +
+                                         4 * (lane & 3)];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int st = 0; st < 2; ++st)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const uint16_t *p = vp + (32 * u + 16 * st) * kValueRow + 32 * d;
+                    const uintx2_t v0 = lds_read_transposed(p);
+                    const uintx2_t v1 = lds_read_transposed(p + 8 * kValueRow);
+                    const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);
+                }
+    };
+    const auto weights = [&](int it) __attribute__((always_inline)) {
+        const int k0 = tile_key(it);
+        // every key of the tile seen by every row of the wave?
+        const bool whole = k0 + KT - 1 <= first &&
+                           (a.window == 0 || k0 > last - a.window || k0 + KT - 1 < a.sinks);
+        if (!whole) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int j = k0 + 32 * u + 8 * (i / 4) + 4 * half + i % 4;
+                    const bool ok = (j <= pos) & ((j > before) | (j < sinks_end));
+                    s[u][i] = ok ? s[u][i] : -INFINITY;
+                }
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
+        mx = max_of_halves(mx) * cs;
+        if (__any(mx > M + kSlack)) {
+            const float M2 = fmaxf(M, mx);
+            const float f = __builtin_amdgcn_exp2f(M - M2);
+            M = M2;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] *= f;
+        }
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            uintx4_t w[2];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], cs, -M));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], cs, -M));
+                w[i / 8][i % 8 / 2] = pack_bf16(p0, p1);
+                l += p0 + p1;
+            }
+            pf[u][0] = __builtin_bit_cast(bf16x8_t, w[0]);
+            pf[u][1] = __builtin_bit_cast(bf16x8_t, w[1]);
         }
     };
-    const auto stage = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = r0 + i * kRowStep;
-            *reinterpret_cast<uintx4_t *>(&sk[buf][r * kKeyRow + 8 * my_chunk]) = rk[i];
-            *reinterpret_cast<uintx4_t *>(&sv[buf][r * kValueRow + 8 * my_chunk]) = rv[i];
-        }
+    // phases A(it), B(it)
+    const auto step = [&](int it, Set &x) __attribute__((always_inline)) {
+        weigh(it);
+        scores(it + 1);
+        stage(it, x);
+        order_phase<SUB * 2 * DT, SUB * KS, (DP > 128 ? AH256 : 4)>();
+        phase_barrier();
+        look_up(tile_at(it + 3 + kDepth));
+        weights(it + 1);
+        phase_barrier();
     };
-    if (n_iter > 0) {
-        look_up(0);
-        fetch(0);
-        look_up(min(1, n_iter - 1));
-        stage(0);
-    }
-    __syncthreads();
 
     if (n_iter > 0) {
-    int it = 0;
-    do {
-        const int buf = it & 1;
+        Set x, y;  // of A(-1), A(1), ..., and of A(0), A(2), ... (one of all with kDepth = 1)
+        Where w;
+        look_up(0);
+        locate(0, w);
+        uintx4_t k0[kLoads];
+        fetch(head_k, w, k0);
+        fetch(head_v, w, x.v);
+        look_up(tile_at(1));
+        locate(tile_at(1), newest);
+        fetch(head_k, newest, x.k);
+        if (kDepth > 1) {
+            fetch(head_v, newest, y.v);
+            look_up(tile_at(2));
+            locate(tile_at(2), newest);
+            fetch(head_k, newest, y.k);
+        }
+        look_up(tile_at(1 + kDepth));
+        put(sk[0], kKeyRow, k0);
+        phase_barrier();
+        if (group > 0) phase_barrier();
+        scores(0);
+        stage(-1, x);
+        phase_barrier();
+        look_up(tile_at(2 + kDepth));
+        weights(0);
+        phase_barrier();
+        Set &next = kDepth > 1 ? y : x;
+        int it = 0;
+        if (n_iter > 2) {
+            do {
+                step(it, next);
+                step(it + 1, x);
+                it += 2;
+            } while (it + 2 < n_iter);
+        }
         if (it + 1 < n_iter) {
-            fetch(it + 1);
-            look_up(min(it + 2, n_iter - 1));
+            step(it, next);
+            ++it;
         }
-        const int k0 = tile_key(it);
-        // any key of the tile that some row of the wave sees?
-        const bool seen = k0 <= last && (a.window == 0 || k0 < a.sinks ||
-                                         k0 + KT - 1 > first - a.window);
-        if (seen) {
-            floatx16_t s[SUB];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                s[u] = floatx16_t(0.0f);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    const bf16x8_t kf = *reinterpret_cast<const bf16x8_t *>(
-                        &sk[buf][(32 * u + (lane & 31)) * kKeyRow + 16 * ks + 8 * half]);
-                    s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kf, qf[ks], s[u], 0, 0, 0);
-                }
-            }
-            // every key of the tile seen by every row of the wave?
-            const bool whole =
-                k0 + KT - 1 <= first &&
-                (a.window == 0 || k0 > last - a.window || k0 + KT - 1 < a.sinks);
-            if (!whole) {
-#pragma unroll
-                for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int j = k0 + 32 * u + 8 * (i / 4) + 4 * half + i % 4;
-                        const bool ok = (j <= pos) & ((j > before) | (j < a.sinks));
-                        s[u][i] = ok ? s[u][i] : -INFINITY;
-                    }
-            }
-            float mx = s[0][0];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
-            mx = fmaxf(mx, other_half(mx)) * cs;
-            if (__any(mx > M + kSlack)) {
-                const float M2 = fmaxf(M, mx);
-                const float f = __builtin_amdgcn_exp2f(M - M2);
-                M = M2;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= f;
-            }
-            bf16x8_t pf[SUB][2];
-#pragma unroll
-            for (int u = 0; u < SUB; ++u) {
-                uintx4_t w[2];
-#pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], cs, -M));
-                    const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], cs, -M));
-                    l += p0 + p1;
-                    w[i / 8][i % 8 / 2] = pack_bf16(p0, p1);
-                }
-                pf[u][0] = __builtin_bit_cast(bf16x8_t, w[0]);
-                pf[u][1] = __builtin_bit_cast(bf16x8_t, w[1]);
-            }
-            // O^T += V^T P^T, 16 keys a step: slots 8 half + 0..3 are keys 4 half + 0..3 of the
-            // step, slots 8 half + 4..7 keys 8 + 4 half + 0..3
-#pragma unroll
-            for (int u = 0; u < SUB; ++u)
-#pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const uint16_t *vp =
-                        &sv[buf][(32 * u + 16 * st + 4 * half + (lane & 15) / 4) * kValueRow +
-                                 (lane & 16) + 4 * (lane & 3)];
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        const uintx2_t v0 = lds_read_transposed(vp + 32 * d);
-                        const uintx2_t v1 = lds_read_transposed(vp + 8 * kValueRow + 32 * d);
-                        const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                            __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);
-                    }
-                }
-        }
-        if (it + 1 < n_iter) stage(buf ^ 1);
-        __syncthreads();
-    } while (++it < n_iter);
+        weigh(it);
+        if (kGroups > 1 && group == 0) phase_barrier();
     }
 
     l += other_half(l);
     if (row >= t.rows) return;
+    const int64_t token = t.q0 + tok, pair = token * a.n_heads + head;
+    if (splits > 1) {
+        const Partials p = partials(a.work, a.T * a.n_heads, splits, part, D);
+        if (half == 0) {
+            p.ml[2 * pair] = M;
+            p.ml[2 * pair + 1] = l;
+        }
+        if (n_iter == 0) return;  // (its sum is 0: the weighted sums are not read)
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int col = 32 * d + 8 * g + 4 * half;
+                if (col < D)
+                    *reinterpret_cast<floatx4_t *>(p.o + pair * D + col) = floatx4_t{
+                        o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+            }
+        return;
+    }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    const int64_t token = t.q0 + tok;
-    if (a.lse && half == 0)
-        a.lse[token * a.n_heads + head] = l > 0.0f ? M * kLn2 + logf(l) : -INFINITY;
+    if (a.lse && half == 0) a.lse[pair] = l > 0.0f ? M * kLn2 + logf(l) : -INFINITY;
     const int64_t base = token * a.ldy + static_cast<int64_t>(head) * D;
     const bool wide = wide_rows(a);
 #pragma unroll
@@ -282,27 +494,105 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
         }
 }
 
+// Joins the splits of a (token row, head), one wave each, in order.
+__global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int D, int n_seqs,
+                                                                int splits) {
+    const int64_t pairs = a.T * a.n_heads;
+    const int64_t pair = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int64_t token = pair / a.n_heads;
+    // (rows that q_start gives to no sequence have no partial results)
+    if (pair >= pairs || token < a.q_start[0] || token >= a.q_start[n_seqs]) return;
+    const int col = 4 * lane;
+    float m = kNoMax, l = 0.0f;
+    floatx4_t v = floatx4_t(0.0f);
+    for (int i = 0; i < splits; ++i) {
+        const Partials p = partials(a.work, pairs, splits, i, D);
+        const float m1 = p.ml[2 * pair], l1 = p.ml[2 * pair + 1];
+        if (l1 == 0.0f) continue;
+        const float m2 = fmaxf(m, m1);
+        const float f = __builtin_amdgcn_exp2f(m - m2), f1 = __builtin_amdgcn_exp2f(m1 - m2);
+        m = m2;
+        l = l * f + l1 * f1;
+        if (col < D) v = v * f + f1 * *reinterpret_cast<const floatx4_t *>(p.o + pair * D + col);
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+    if (a.lse && lane == 0) a.lse[pair] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+    if (col < D)
+        store_out4(a.y, token * a.ldy + (pair - token * a.n_heads) * D + col, v * inv, a.out_f32,
+                   wide_rows(a));
+}
+
+struct Plan {
+    int nw, splits;
+    int64_t tiles;  // at most this many tiles of rows: every sequence rounds up once
+};
+#ifndef SMALLF
+#define SMALLF 2
+#endif
+Plan plan_of(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
+    const int64_t G = n_heads / c.n_kv, cus = device_cu_count();
+    Plan p;
+    p.nw = (T * G / 256 + c.n_seqs) * c.n_kv < SMALLF * cus ? 4 : 8;
+    p.tiles = T * G / (32 * p.nw) + c.n_seqs;
+    const int64_t blocks = p.tiles * c.n_kv;
+    int64_t keys = c.capacity;
+    if (window > 0 && int64_t(window) + sinks + 32 * p.nw < keys)
+        keys = int64_t(window) + sinks + 32 * p.nw;
+    const int64_t key_tiles = (keys + 63) / 64;
+    p.splits = 1;
+    if (blocks < cus && key_tiles >= 8) {
+        const int64_t most = key_tiles / 4 < 64 ? key_tiles / 4 : 64;
+        p.splits = static_cast<int>(2 * cus / blocks < most ? 2 * cus / blocks : most);
+    }
+    return p;
+}
+
 template <int DP, int NW, int KT>
-void launch(const AttnArgs &a, const KvView &c, hipStream_t stream) {
-    const int64_t G = a.n_heads / c.n_kv;
-    // at most this many tiles: every sequence rounds up once
-    const int64_t tiles = a.T * G / (NW * 32) + c.n_seqs;
-    const dim3 grid(static_cast<unsigned>(tiles * c.n_kv));
-    hipLaunchKernelGGL((attn_prefill_kernel<DP, NW, KT>), grid, dim3(NW * 64), 0, stream, a, c,
-                       static_cast<int>(tiles));
+void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t stream) {
+    const dim3 grid(static_cast<unsigned>(p.tiles * c.n_kv * p.splits));
+    if (c.page_mask >= KT - 1)
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, NW, KT, kTilePages>), grid, dim3(NW * 64), 0,
+                           stream, a, c, p.splits);
+    else if (c.page_mask >= 7)
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, NW, KT, kSpanPages>), grid, dim3(NW * 64), 0,
+                           stream, a, c, p.splits);
+    else
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, NW, KT, kAnyPages>), grid, dim3(NW * 64), 0,
+                           stream, a, c, p.splits);
+}
+
+template <int DP, int KT>
+void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t stream) {
+    if (p.nw == 8)
+        launch<DP, 8, KT>(p, a, c, stream);
+    else
+        launch<DP, 4, KT>(p, a, c, stream);
 }
 
 }  // namespace
 
-size_t attn_prefill_work_bytes(int64_t, int, const KvView &, int, int) { return 0; }
+size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
+    const Plan p = plan_of(T, n_heads, c, window, sinks);
+    if (p.splits == 1) return 0;
+    return sizeof(float) * p.splits * T * n_heads * (c.head_dim + 2);
+}
 
 hipError_t launch_attn_prefill(const AttnArgs &a, const KvView &c, hipStream_t stream) {
+    const Plan p = plan_of(a.T, a.n_heads, c, a.window, a.sinks);
     if (c.head_dim <= 64)
-        launch<64, 8, 64>(a, c, stream);
+        launch<64, 64>(p, a, c, stream);
     else if (c.head_dim <= 128)
-        launch<128, 8, 64>(a, c, stream);
+        launch<128, 64>(p, a, c, stream);
     else
-        launch<256, 8, 32>(a, c, stream);
+        launch<256, 32>(p, a, c, stream);
+    if (p.splits > 1) {
+        const hipError_t err = hipGetLastError();
+        if (err != hipSuccess) return err;
+        const int64_t pairs = a.T * a.n_heads;
+        hipLaunchKernelGGL(attn_prefill_join_kernel, dim3(static_cast<unsigned>((pairs + 3) / 4)),
+                           dim3(256), 0, stream, a, c.head_dim, c.n_seqs, p.splits);
+    }
     return hipGetLastError();
 }
 
