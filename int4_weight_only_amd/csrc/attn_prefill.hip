@@ -16,6 +16,8 @@
 // The running maximum M (in units of log2) is only raised when a tile exceeds it by more than 2^8:
 // the weights then stay below 2^8 and keep their relative precision, and the accumulators are
 // rarely rescaled.
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace w4 {
@@ -23,8 +25,11 @@ namespace w4 {
 namespace {
 
 constexpr int kSlack = 8;
-#ifndef AH256
-#define AH256 2
+#ifndef VG
+#define VG 2
+#endif
+#ifndef AHEAD
+#define AHEAD 4
 #endif
 
 // A block's rows: of sequence `seq`, stacked rows row0 .. row0 + BM - 1 of `rows`; token row q0 and
@@ -97,26 +102,37 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
 }
 
 // Orders a multiplying phase: NV products with value fragments (two LDS reads each), then NK with
-// key fragments (one each), every read AHEAD products before its use. (Left to itself the scheduler
-// keeps two fragments in flight, and a product waits for most of an LDS read.)
-template <int NV, int NK, int AHEAD>
+// key fragments (one each), every read NAHEAD products before its use, a few other vector
+// instructions between. (Left to itself the scheduler keeps two fragments in flight, where a product
+// waits for most of an LDS read.)
+template <int NV, int NK, int NAHEAD>
 __device__ __forceinline__ void order_phase() {
-    constexpr int kMfma = 0x008, kLdsRead = 0x100;
-    __builtin_amdgcn_sched_group_barrier(kLdsRead, 2 * AHEAD, 0);
+    constexpr int kVector = 0x002, kMatrix = 0x008, kLdsRead = 0x100;
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, 2 * NAHEAD, 0);
 #pragma unroll
     for (int i = 0; i < NV + NK; ++i) {
-        __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-        if (i + AHEAD < NV)
+        __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
+        if (i + NAHEAD < NV)
             __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
-        else if (i + AHEAD < NV + NK)
+        else if (i + NAHEAD < NV + NK)
             __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
+        if (VG) __builtin_amdgcn_sched_group_barrier(kVector, VG, 0);
     }
 }
 
-// Barrier between phases, after this wave's LDS accesses; loads from memory stay in flight.
+// s_waitcnt immediate: vmcnt(N), the other counters not waited for.
+template <int N>
+constexpr int wait_vm() {
+    return (N & 0xF) | (N >> 4) << 14 | 0x7 << 4 | 0xF << 8;
+}
+
+// Barrier between phases, after this wave's LDS accesses. What it sent for from memory may stay on
+// its way, unless LANDED.
+template <bool LANDED>
 __device__ __forceinline__ void phase_barrier() {
     phase_fence();
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); vmcnt and expcnt not waited for
+    if (LANDED) __builtin_amdgcn_s_waitcnt(wait_vm<0>());
+    __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     phase_fence();
 }
@@ -132,24 +148,59 @@ __device__ __forceinline__ Partials partials(void *work, int64_t pairs, int spli
     return {base + part * pairs * D, base + splits * pairs * D + part * pairs * 2};
 }
 
+// A tile in LDS: direct loads from memory, which lay 64 lanes of 16 bytes down in a row, put kSpan
+// consecutive rows of DP elements into a block of 1 KiB; blocks follow each other with a gap. Inside
+// a row the 16-byte chunks are permuted (by the choice of what each lane loads), so that neither the
+// key fragments (one chunk of 16 or 32 consecutive rows) nor the transposed value reads (32 bytes of
+// 4 consecutive rows) meet in the same of the 64 banks: chunk c of row r is at place
+//   c ^ key_swap(r) for keys,   c ^ 2 value_swap(r) for values,
+// rows of 128, 256 and 512 bytes covering 2, 1 and 1/2 of a row of banks.
+template <int DP>
+struct TileLayout {
+    static constexpr int kSpan = 512 / DP;
+    static constexpr int kKeyBlock = 512 + (DP > 128 ? 16 : 32);   // elements from block to block
+    static constexpr int kValueBlock = 512 + (DP > 128 ? 32 : 0);
+    __device__ static int key_swap(int r) { return DP > 128 ? r & 1 : DP > 64 ? r & 3 : r >> 1 & 3; }
+    __device__ static int value_swap(int r) {
+        return DP > 128 ? r & 1 : DP > 64 ? r & 3 : r >> 1 & 1;
+    }
+    // Element offset of chunk c (of values: of the first chunk of pair c / 2) of row r.
+    __device__ static int key_at(int r, int c) {
+        return r / kSpan * kKeyBlock + r % kSpan * DP + 8 * (c ^ key_swap(r));
+    }
+    __device__ static int value_at(int r, int c) {
+        return r / kSpan * kValueBlock + r % kSpan * DP + 8 * (c ^ 2 * value_swap(r));
+    }
+};
+
+// 16 bytes per lane from memory to LDS, lane l's at lds + 16 l.
+__device__ __forceinline__ void load_to_lds(const void *from, uint16_t *lds) {
+    typedef const __attribute__((address_space(1))) void *global_t;
+    typedef __attribute__((address_space(3))) void *lds_t;
+    __builtin_amdgcn_global_load_lds((global_t)from, (lds_t)lds, 16, 0, 0);
+}
+
 // What lies in one page: a tile (pages of KT slots and more), the rows a wave stages in one
 // instruction (8 at most, aligned: pages of 8 slots and more), or a row.
 enum { kAnyPages = 0, kSpanPages = 1, kTilePages = 2 };
 
 template <int DP, int NW, int KT, int PAGES>
 __global__ void __launch_bounds__(NW * 64)
-__attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c, int splits) {
+__attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvView c, int splits) {
     constexpr int BM = NW * 32;
     constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
     constexpr int kSpan = 64 / kChunks;                // rows a wave stages in one instruction
     constexpr int kLoads = KT / (NW * kSpan);          // instructions a wave stages a tile with
     static_assert(kLoads * NW * kSpan == KT, "every wave stages the same number of rows");
-    constexpr int kDepth = DP > 128 || (DP > 64 && NW == 4) ? 1 : 2;           // tiles in flight (registers decide)
-    constexpr int kKeyRow = Rows<DP>::kKey, kValueRow = Rows<DP>::kValue;
+    using L = TileLayout<DP>;
     constexpr int DT = DP / 32, KS = DP / 16, SUB = KT / 32;
     constexpr int kGroups = NW / 4;
-    __shared__ __attribute__((aligned(16))) uint16_t sk[2][KT * kKeyRow];
-    __shared__ __attribute__((aligned(16))) uint16_t sv[2][KT * kValueRow];
+    // (arrays of their own: the compiler then sees that a direct load on its way into one does not
+    // touch the others, and does not wait for it before it reads them)
+    __shared__ __attribute__((aligned(16))) uint16_t sk0[KT / kSpan * L::kKeyBlock];
+    __shared__ __attribute__((aligned(16))) uint16_t sk1[KT / kSpan * L::kKeyBlock];
+    __shared__ __attribute__((aligned(16))) uint16_t sv0[KT / kSpan * L::kValueBlock];
+    __shared__ __attribute__((aligned(16))) uint16_t sv1[KT / kSpan * L::kValueBlock];
 
     const int lane = threadIdx.x & 63;
     const int wid = uniform(threadIdx.x >> 6);
@@ -209,7 +260,9 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     // whose key no row of the block sees is read from one that some row sees (finite; its weights are
     // 0; of the same rows, if there is any); dims past D from the row's last chunk (they meet zeros of
     // q, or outputs that are not kept).
-    const int my_row = lane / kChunks, my_col = min(8 * (lane % kChunks), D - 8);
+    const int my_row = lane / kChunks;
+    const int k_col = min(8 * (lane % kChunks ^ L::key_swap(my_row)), D - 8);
+    const int v_col = min(8 * (lane % kChunks ^ 2 * L::value_swap(my_row)), D - 8);
     const int32_t *table = c.table + t.seq * c.ld_table;
     const uint16_t *head_k = c.k + static_cast<int64_t>(hk) * c.head_stride;
     const uint16_t *head_v = c.v + static_cast<int64_t>(hk) * c.head_stride;
@@ -237,7 +290,7 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
     uint32_t seen_off[kLoads];  // the offsets in a tile whose rows are all seen
 #pragma unroll
     for (int i = 0; i < kLoads; ++i)
-        seen_off[i] = ((PAGES == kTilePages ? span_at(i) : 0) + my_row) * c.slot_stride + my_col;
+        seen_off[i] = ((PAGES == kTilePages ? span_at(i) : 0) + my_row) * c.slot_stride;
     int entry[kBases];
     const auto look_up = [&](int it) {  // the page table entries of a tile
         const int k0 = tile_key(it);
@@ -258,7 +311,7 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
             w.base[0] = page_offset(entry[0]) +
                         static_cast<int64_t>((k0 & c.page_mask) * c.slot_stride);
             const int safe = k0 < sinks_end ? k0 : max(k0, lo);
-            const uint32_t other = (safe - k0) * c.slot_stride + my_col;
+            const uint32_t other = (safe - k0) * c.slot_stride;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
                 w.off[i] = visible(k0 + span_at(i) + my_row) ? seen_off[i] : other;
@@ -274,60 +327,50 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
                     const int first_row = safe >= s0 && safe < s0 + kSpan ? s0 : safe;
                     w.base[i] = page_offset(entry[i]) +
                                 static_cast<int64_t>((first_row & c.page_mask) * c.slot_stride);
-                    w.off[i] = vis ? seen_off[i] : (safe - first_row) * c.slot_stride + my_col;
+                    w.off[i] = vis ? seen_off[i] : (safe - first_row) * c.slot_stride;
                 } else {
                     const int from = vis ? p : safe;
                     w.base[i] = page_offset(read_const(table + (from >> c.page_shift)));
-                    w.off[i] = (from & c.page_mask) * c.slot_stride + my_col;
+                    w.off[i] = (from & c.page_mask) * c.slot_stride;
                 }
             }
         }
     };
-    const auto fetch = [&](const uint16_t *kv, const Where &w, uintx4_t *r) {
+    const auto fetch = [&](const uint16_t *kv, const Where &w, int col, uint16_t *dst, int block)
+                           __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            r[i] = *reinterpret_cast<const uintx4_t *>(
-                reinterpret_cast<const char *>(kv + w.base[PAGES == kTilePages ? 0 : i]) +
-                2u * w.off[i]);
+            load_to_lds(reinterpret_cast<const char *>(kv + w.base[PAGES == kTilePages ? 0 : i]) +
+                            2u * (w.off[i] + col),
+                        dst + (i * NW + wid) * block);
     };
-    const auto put = [&](uint16_t *dst, int stride, const uintx4_t *r) {
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            *reinterpret_cast<uintx4_t *>(
-                &dst[(span_at(i) + my_row) * stride + 8 * (lane % kChunks)]) = r[i];
-    };
-    // Rows on their way. Phase A(i) stages the keys of tile i + 2 and the values of tile i + 1, and
-    // sends for the keys of tile i + 2 + kDepth and the values of the tile before that in their place.
-    // (Past the last tile both repeat it, into buffers that nothing reads any more.)
-    struct Set {
-        uintx4_t k[kLoads], v[kLoads];
-    };
-    Where newest;  // of the newest tile whose keys were sent for
+    // Sends for the keys of tile it + 2 and the values of tile it + 1, whose rows were found for its
+    // keys. (Past the last tile both repeat it, into buffers that nothing reads any more.)
+    Where newest;  // of tile it + 1
     const auto tile_at = [&](int it) { return min(it, n_iter - 1); };
-    const auto stage = [&](int it, Set &x) __attribute__((always_inline)) {
-        put(sk[it & 1], kKeyRow, x.k);
-        put(sv[(it + 1) & 1], kValueRow, x.v);
-        fetch(head_v, newest, x.v);
-        locate(tile_at(it + 2 + kDepth), newest);
-        fetch(head_k, newest, x.k);
+    const auto send = [&](int it, uint16_t *k, uint16_t *v) __attribute__((always_inline)) {
+        fetch(head_v, newest, v_col, v, L::kValueBlock);
+        locate(tile_at(it + 2), newest);
+        fetch(head_k, newest, k_col, k, L::kKeyBlock);
+        look_up(tile_at(it + 3));
     };
 
     // The two products and the softmax of a tile alternate with a barrier between them: phase A
-    // multiplies (the values of tile i, the keys of tile i + 1) and stages, phase B turns the scores
-    // into weights. With two groups of four waves (one of each on every SIMD), the second runs one
-    // phase behind the first, so that one multiplies while the other computes weights.
+    // multiplies (the values of tile i, the keys of tile i + 1), phase B turns the scores into
+    // weights. With two groups of four waves (one of each on every SIMD), the second runs one phase
+    // behind the first, so that one multiplies while the other computes weights.
     //   phase        0        1        2        3
     //   group 0      A(-1)    B(-1)    A(0)     B(0)  ...
     //   group 1               A(-1)    B(-1)    A(0)  ...
-    // A(i) reads keys i + 1 and values i and writes keys i + 2 and values i + 1 into the other buffers:
-    // group 0's A(i) comes after the last phase that reads what was there (group 1's A(i - 1)), group
-    // 1's A(i) before the first that reads the new (group 0's A(i + 1)).
-    const int group = kGroups > 1 ? wid / 4 : 0;
+    // send(i) overwrites the buffers of keys i and values i - 1, last read in group 1's A(i - 1). Both
+    // groups send in the phase after that, which is group 0's A(i) and group 1's B(i - 1), and wait
+    // at the end of the next one, before group 0's A(i + 1) reads.
     floatx16_t s[SUB];
     bf16x8_t pf[SUB][2];
 
-    const auto scores = [&](int it) __attribute__((always_inline)) {
-        const uint16_t *kp = &sk[it & 1][(lane & 31) * kKeyRow + 8 * half];
+    const auto scores = [&](const uint16_t *k) __attribute__((always_inline)) {
+        // (chunks 2 ks + half, swapped: even and odd steps each at constant offsets)
+        const uint16_t *kp[2] = {k + L::key_at(lane & 31, half), k + L::key_at(lane & 31, 2 + half)};
 #pragma unroll
         for (int u = 0; u < SUB; ++u) s[u] = floatx16_t(0.0f);
 #pragma unroll
@@ -335,23 +378,27 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
                 s[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    *reinterpret_cast<const bf16x8_t *>(kp + 32 * u * kKeyRow + 16 * ks), qf[ks],
-                    s[u], 0, 0, 0);
+                    *reinterpret_cast<const bf16x8_t *>(kp[ks & 1] + 32 * u / kSpan * L::kKeyBlock +
+                                                        ks / 2 * 32),
+                    qf[ks], s[u], 0, 0, 0);
     };
     // O^T += V^T P^T, 16 keys a step: slots 8 half + 0..3 are keys 4 half + 0..3 of the step, slots
     // 8 half + 4..7 keys 8 + 4 half + 0..3
-    const auto weigh = [&](int it) __attribute__((always_inline)) {
-        const uint16_t *vp = &sv[it & 1][(4 * half + (lane & 15) / 4) * kValueRow + (lane & 16) +
-                                         4 * (lane & 3)];
+    const auto weigh = [&](const uint16_t *v) __attribute__((always_inline)) {
+        // (chunk pair 2 d + lane / 16 % 2 of a row, swapped: even and odd d at constant offsets)
+        const int r = 4 * half + (lane & 15) / 4, pair = lane >> 4 & 1, in = 4 * (lane & 3);
+        const uint16_t *vp[2] = {v + L::value_at(r, 2 * pair) + in,
+                                 v + L::value_at(r, 2 * pair + 4) + in};
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int st = 0; st < 2; ++st)
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
-                    const uint16_t *p = vp + (32 * u + 16 * st) * kValueRow + 32 * d;
+                    const uint16_t *p =
+                        vp[d & 1] + (32 * u + 16 * st) / kSpan * L::kValueBlock + d / 2 * 64;
                     const uintx2_t v0 = lds_read_transposed(p);
-                    const uintx2_t v1 = lds_read_transposed(p + 8 * kValueRow);
+                    const uintx2_t v1 = lds_read_transposed(p + 8 / kSpan * L::kValueBlock);
                     const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
                     o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
                         __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);
@@ -363,12 +410,15 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
         const bool whole = k0 + KT - 1 <= first &&
                            (a.window == 0 || k0 > last - a.window || k0 + KT - 1 < a.sinks);
         if (!whole) {
+            // key i of the lane's is at place 32 u + 8 (i / 4) + i % 4 of those from k0 + 4 half on
+            const int base = k0 + 4 * half;
+            const int newest_at = pos - base, before_at = before - base, sinks_at = sinks_end - base;
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int j = k0 + 32 * u + 8 * (i / 4) + 4 * half + i % 4;
-                    const bool ok = (j <= pos) & ((j > before) | (j < sinks_end));
+                    const int at = 32 * u + 8 * (i / 4) + i % 4;
+                    const bool ok = (at <= newest_at) & ((at > before_at) | (at < sinks_at));
                     s[u][i] = ok ? s[u][i] : -INFINITY;
                 }
         }
@@ -400,60 +450,61 @@ __attribute__((amdgpu_waves_per_eu(2))) attn_prefill_kernel(AttnArgs a, KvView c
             pf[u][1] = __builtin_bit_cast(bf16x8_t, w[1]);
         }
     };
-    // phases A(it), B(it)
-    const auto step = [&](int it, Set &x) __attribute__((always_inline)) {
-        weigh(it);
-        scores(it + 1);
-        stage(it, x);
-        order_phase<SUB * 2 * DT, SUB * KS, (DP > 128 ? AH256 : 4)>();
-        phase_barrier();
-        look_up(tile_at(it + 3 + kDepth));
-        weights(it + 1);
-        phase_barrier();
-    };
-
-    if (n_iter > 0) {
-        Set x, y;  // of A(-1), A(1), ..., and of A(0), A(2), ... (one of all with kDepth = 1)
-        Where w;
-        look_up(0);
-        locate(0, w);
-        uintx4_t k0[kLoads];
-        fetch(head_k, w, k0);
-        fetch(head_v, w, x.v);
-        look_up(tile_at(1));
-        locate(tile_at(1), newest);
-        fetch(head_k, newest, x.k);
-        if (kDepth > 1) {
-            fetch(head_v, newest, y.v);
-            look_up(tile_at(2));
-            locate(tile_at(2), newest);
-            fetch(head_k, newest, y.k);
-        }
-        look_up(tile_at(1 + kDepth));
-        put(sk[0], kKeyRow, k0);
-        phase_barrier();
-        if (group > 0) phase_barrier();
-        scores(0);
-        stage(-1, x);
-        phase_barrier();
-        look_up(tile_at(2 + kDepth));
+    // Both groups' phases (the group as a constant: the compiler then knows what is on its way where).
+    const auto run = [&](auto group_number) __attribute__((always_inline)) {
+        constexpr int group = decltype(group_number)::value;
+        // phases A(it), B(it); k and v: the buffers of tile it, k1 and v1: of tile it + 1
+        const auto step = [&](int it, uint16_t *k, uint16_t *v, uint16_t *k1, uint16_t *v1)
+                              __attribute__((always_inline)) {
+            if constexpr (group == 0) send(it, k, v1);
+            phase_fence();
+            weigh(v);
+            scores(k1);
+            order_phase<SUB * 2 * DT, SUB * KS, AHEAD>();
+            phase_barrier<group == 1>();
+            if constexpr (group == 1) send(it + 1, k1, v);
+            weights(it + 1);
+            phase_barrier<group == 0>();
+        };
+        if constexpr (group == 1) phase_barrier<false>();
+        scores(sk0);
+        phase_barrier<group == 1>();
+        if constexpr (group == 1) send(0, sk0, sv1);
         weights(0);
-        phase_barrier();
-        Set &next = kDepth > 1 ? y : x;
+        phase_barrier<group == 0>();
         int it = 0;
         if (n_iter > 2) {
             do {
-                step(it, next);
-                step(it + 1, x);
+                step(it, sk0, sv0, sk1, sv1);
+                step(it + 1, sk1, sv1, sk0, sv0);
                 it += 2;
             } while (it + 2 < n_iter);
         }
         if (it + 1 < n_iter) {
-            step(it, next);
+            step(it, sk0, sv0, sk1, sv1);
             ++it;
         }
-        weigh(it);
-        if (kGroups > 1 && group == 0) phase_barrier();
+        weigh(it & 1 ? sv1 : sv0);
+        // nothing of this wave's is on its way to LDS when it ends
+        __builtin_amdgcn_s_waitcnt(wait_vm<0>());
+        if constexpr (group == 0) phase_barrier<false>();  // (as many as group 1)
+    };
+
+    if (n_iter > 0) {
+        look_up(0);
+        locate(0, newest);
+        fetch(head_k, newest, k_col, sk0, L::kKeyBlock);
+        phase_fence();
+        look_up(tile_at(1));
+        send(-1, sk1, sv0);
+        // (every wave's keys 0 have landed; the rest has time until A(0))
+        phase_fence();
+        __builtin_amdgcn_s_waitcnt(wait_vm<2 * kLoads>());
+        phase_barrier<false>();
+        if (kGroups == 1 || wid < 4)
+            run(std::integral_constant<int, 0>{});
+        else
+            run(std::integral_constant<int, 1>{});
     }
 
     l += other_half(l);
