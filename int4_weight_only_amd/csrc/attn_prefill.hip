@@ -24,9 +24,16 @@ namespace w4 {
 
 namespace {
 
+constexpr int kWaves = 4, kTileRows = 32 * kWaves;
 constexpr int kSlack = 8;
 #ifndef VG
-#define VG 2
+#define VG 0
+#endif
+#ifndef OVER
+#define OVER 1
+#endif
+#ifndef AHEADV
+#define AHEADV 3
 #endif
 #ifndef AHEAD
 #define AHEAD 4
@@ -101,22 +108,19 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
     return false;
 }
 
-// Orders a multiplying phase: NV products with value fragments (two LDS reads each), then NK with
-// key fragments (one each), every read NAHEAD products before its use, a few other vector
-// instructions between. (Left to itself the scheduler keeps two fragments in flight, where a product
-// waits for most of an LDS read.)
-template <int NV, int NK, int NAHEAD>
-__device__ __forceinline__ void order_phase() {
+// Orders a run of N products, each with READS LDS reads for its fragment, every fragment read
+// NAHEAD products before its use, and VECTOR vector instructions after each product. (Left to itself
+// the scheduler keeps two fragments in flight, where a product waits for most of an LDS read, and
+// computes the weights before the products.)
+template <int N, int READS, int NAHEAD, int VECTOR>
+__device__ __forceinline__ void order_products() {
     constexpr int kVector = 0x002, kMatrix = 0x008, kLdsRead = 0x100;
-    __builtin_amdgcn_sched_group_barrier(kLdsRead, 2 * NAHEAD, 0);
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, READS * NAHEAD, 0);
 #pragma unroll
-    for (int i = 0; i < NV + NK; ++i) {
+    for (int i = 0; i < N; ++i) {
         __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
-        if (i + NAHEAD < NV)
-            __builtin_amdgcn_sched_group_barrier(kLdsRead, 2, 0);
-        else if (i + NAHEAD < NV + NK)
-            __builtin_amdgcn_sched_group_barrier(kLdsRead, 1, 0);
-        if (VG) __builtin_amdgcn_sched_group_barrier(kVector, VG, 0);
+        if (i + NAHEAD < N) __builtin_amdgcn_sched_group_barrier(kLdsRead, READS, 0);
+        if constexpr (VECTOR > 0) __builtin_amdgcn_sched_group_barrier(kVector, VECTOR, 0);
     }
 }
 
@@ -126,13 +130,10 @@ constexpr int wait_vm() {
     return (N & 0xF) | (N >> 4) << 14 | 0x7 << 4 | 0xF << 8;
 }
 
-// Barrier between phases, after this wave's LDS accesses. What it sent for from memory may stay on
-// its way, unless LANDED.
-template <bool LANDED>
-__device__ __forceinline__ void phase_barrier() {
+// Barrier after a tile: this wave's LDS reads are done, what it sent for has landed.
+__device__ __forceinline__ void tile_barrier() {
     phase_fence();
-    if (LANDED) __builtin_amdgcn_s_waitcnt(wait_vm<0>());
-    __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(wait_vm<0>() & 0xF0FF);  // vmcnt(0) and lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     phase_fence();
 }
@@ -153,23 +154,24 @@ __device__ __forceinline__ Partials partials(void *work, int64_t pairs, int spli
 // a row the 16-byte chunks are permuted (by the choice of what each lane loads), so that neither the
 // key fragments (one chunk of 16 or 32 consecutive rows) nor the transposed value reads (32 bytes of
 // 4 consecutive rows) meet in the same of the 64 banks: chunk c of row r is at place
-//   c ^ key_swap(r) for keys,   c ^ 2 value_swap(r) for values,
-// rows of 128, 256 and 512 bytes covering 2, 1 and 1/2 of a row of banks.
+//   c ^ key_swap(r) for keys,   c ^ 4 value_swap(r) for values,
+// rows of 128, 256 and 512 bytes covering 1/2, 1 and 2 rows of banks.
 template <int DP>
 struct TileLayout {
     static constexpr int kSpan = 512 / DP;
     static constexpr int kKeyBlock = 512 + (DP > 128 ? 16 : 32);   // elements from block to block
-    static constexpr int kValueBlock = 512 + (DP > 128 ? 32 : 0);
+    static constexpr int kValueBlock = 512 + (DP > 128 ? 64 : 0);
+    static constexpr int kValueSwaps = DP == 128 ? 4 : 2;  // values that value_swap takes
     __device__ static int key_swap(int r) { return DP > 128 ? r & 1 : DP > 64 ? r & 3 : r >> 1 & 3; }
     __device__ static int value_swap(int r) {
         return DP > 128 ? r & 1 : DP > 64 ? r & 3 : r >> 1 & 1;
     }
-    // Element offset of chunk c (of values: of the first chunk of pair c / 2) of row r.
+    // Element offset of chunk c of row r.
     __device__ static int key_at(int r, int c) {
         return r / kSpan * kKeyBlock + r % kSpan * DP + 8 * (c ^ key_swap(r));
     }
     __device__ static int value_at(int r, int c) {
-        return r / kSpan * kValueBlock + r % kSpan * DP + 8 * (c ^ 2 * value_swap(r));
+        return r / kSpan * kValueBlock + r % kSpan * DP + 8 * (c ^ 4 * value_swap(r));
     }
 };
 
@@ -184,17 +186,16 @@ __device__ __forceinline__ void load_to_lds(const void *from, uint16_t *lds) {
 // instruction (8 at most, aligned: pages of 8 slots and more), or a row.
 enum { kAnyPages = 0, kSpanPages = 1, kTilePages = 2 };
 
-template <int DP, int NW, int KT, int PAGES>
-__global__ void __launch_bounds__(NW * 64)
+template <int DP, int KT, int PAGES>
+__global__ void __launch_bounds__(kWaves * 64)
 __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvView c, int splits) {
-    constexpr int BM = NW * 32;
+    constexpr int BM = kTileRows, NW = kWaves;
     constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
     constexpr int kSpan = 64 / kChunks;                // rows a wave stages in one instruction
     constexpr int kLoads = KT / (NW * kSpan);          // instructions a wave stages a tile with
     static_assert(kLoads * NW * kSpan == KT, "every wave stages the same number of rows");
     using L = TileLayout<DP>;
     constexpr int DT = DP / 32, KS = DP / 16, SUB = KT / 32;
-    constexpr int kGroups = NW / 4;
     // (arrays of their own: the compiler then sees that a direct load on its way into one does not
     // touch the others, and does not wait for it before it reads them)
     __shared__ __attribute__((aligned(16))) uint16_t sk0[KT / kSpan * L::kKeyBlock];
@@ -262,7 +263,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
     // q, or outputs that are not kept).
     const int my_row = lane / kChunks;
     const int k_col = min(8 * (lane % kChunks ^ L::key_swap(my_row)), D - 8);
-    const int v_col = min(8 * (lane % kChunks ^ 2 * L::value_swap(my_row)), D - 8);
+    const int v_col = min(8 * (lane % kChunks ^ 4 * L::value_swap(my_row)), D - 8);
     const int32_t *table = c.table + t.seq * c.ld_table;
     const uint16_t *head_k = c.k + static_cast<int64_t>(hk) * c.head_stride;
     const uint16_t *head_v = c.v + static_cast<int64_t>(hk) * c.head_stride;
@@ -355,18 +356,12 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         look_up(tile_at(it + 3));
     };
 
-    // The two products and the softmax of a tile alternate with a barrier between them: phase A
-    // multiplies (the values of tile i, the keys of tile i + 1), phase B turns the scores into
-    // weights. With two groups of four waves (one of each on every SIMD), the second runs one phase
-    // behind the first, so that one multiplies while the other computes weights.
-    //   phase        0        1        2        3
-    //   group 0      A(-1)    B(-1)    A(0)     B(0)  ...
-    //   group 1               A(-1)    B(-1)    A(0)  ...
-    // send(i) overwrites the buffers of keys i and values i - 1, last read in group 1's A(i - 1). Both
-    // groups send in the phase after that, which is group 0's A(i) and group 1's B(i - 1), and wait
-    // at the end of the next one, before group 0's A(i + 1) reads.
+    // An iteration multiplies the keys of tile i + 1, then the values of tile i while the scores of
+    // tile i + 1 become weights (vector instructions between the products), so that the matrix cores
+    // work through the softmax. send(i) overwrites the buffers of keys i and values i - 1, read in the
+    // iteration before, and has the iteration to land: one barrier a tile.
     floatx16_t s[SUB];
-    bf16x8_t pf[SUB][2];
+    bf16x8_t pf[SUB][2];  // the weights of the tile whose values come next
 
     const auto scores = [&](const uint16_t *k) __attribute__((always_inline)) {
         // (chunks 2 ks + half, swapped: even and odd steps each at constant offsets)
@@ -385,10 +380,13 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
     // O^T += V^T P^T, 16 keys a step: slots 8 half + 0..3 are keys 4 half + 0..3 of the step, slots
     // 8 half + 4..7 keys 8 + 4 half + 0..3
     const auto weigh = [&](const uint16_t *v) __attribute__((always_inline)) {
-        // (chunk pair 2 d + lane / 16 % 2 of a row, swapped: even and odd d at constant offsets)
-        const int r = 4 * half + (lane & 15) / 4, pair = lane >> 4 & 1, in = 4 * (lane & 3);
-        const uint16_t *vp[2] = {v + L::value_at(r, 2 * pair) + in,
-                                 v + L::value_at(r, 2 * pair + 4) + in};
+        // (chunk 4 d + 2 (lane / 16 % 2) + (lane & 3) / 2 of a row, swapped: an address for each d
+        // modulo the swaps, constant offsets beyond)
+        constexpr int N = L::kValueSwaps;
+        const int r = 4 * half + (lane & 15) / 4, c = 2 * (lane >> 4 & 1) + (lane & 3) / 2;
+        const uint16_t *vp[N];
+#pragma unroll
+        for (int d = 0; d < N; ++d) vp[d] = v + L::value_at(r, 4 * d + c) + 4 * (lane & 1);
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -396,7 +394,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
 #pragma unroll
                 for (int d = 0; d < DT; ++d) {
                     const uint16_t *p =
-                        vp[d & 1] + (32 * u + 16 * st) / kSpan * L::kValueBlock + d / 2 * 64;
+                        vp[d % N] + (32 * u + 16 * st) / kSpan * L::kValueBlock + d / N * N * 32;
                     const uintx2_t v0 = lds_read_transposed(p);
                     const uintx2_t v1 = lds_read_transposed(p + 8 / kSpan * L::kValueBlock);
                     const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
@@ -404,7 +402,9 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
                         __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);
                 }
     };
-    const auto weights = [&](int it) __attribute__((always_inline)) {
+    // Hides the scores of the keys that a row does not see, and raises M; returns the factor that the
+    // sums so far have to take if it rose for any row (`rose`).
+    const auto raise = [&](int it, bool *rose) __attribute__((always_inline)) {
         const int k0 = tile_key(it);
         // every key of the tile seen by every row of the wave?
         const bool whole = k0 + KT - 1 <= first &&
@@ -428,50 +428,79 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
 #pragma unroll
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
         mx = max_of_halves(mx) * cs;
-        if (__any(mx > M + kSlack)) {
+        float f = 1.0f;
+        *rose = __any(mx > M + kSlack);
+        if (*rose) {
             const float M2 = fmaxf(M, mx);
-            const float f = __builtin_amdgcn_exp2f(M - M2);
+            f = __builtin_amdgcn_exp2f(M - M2);
             M = M2;
             l *= f;
+        }
+        return f;
+    };
+    const auto weights = [&](bf16x8_t (&w)[SUB][2]) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+            uintx4_t x[2];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], cs, -M));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], cs, -M));
+                l += p0 + p1;
+                x[i / 8][i % 8 / 2] = pack_bf16(p0, p1);
+            }
+            w[u][0] = __builtin_bit_cast(bf16x8_t, x[0]);
+            w[u][1] = __builtin_bit_cast(bf16x8_t, x[1]);
+        }
+    };
+
+    // k and v: the buffers of tile it, k1 and v1: of tile it + 1
+    const auto step = [&](int it, uint16_t *k, uint16_t *v, uint16_t *k1, uint16_t *v1)
+                          __attribute__((always_inline)) {
+        send(it, k, v1);
+        scores(k1);
+        order_products<SUB * KS, 1, AHEAD, 0>();
+        bool rose;
+        const float f = raise(it + 1, &rose);
+        // (at 256 dims the registers do not hold both tiles' weights: the softmax after the products)
+        constexpr bool kOver = DP <= 128 && OVER;
+        bf16x8_t next[SUB][2];
+        weigh(v);
+        if constexpr (kOver) weights(next);
+        order_products<SUB * 2 * DT, 2, AHEADV, kOver ? VG : 0>();
+        if constexpr (!kOver) {
+            phase_fence();
+            weights(next);
+        }
+        if (rose) {
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= f;
         }
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
-            uintx4_t w[2];
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], cs, -M));
-                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], cs, -M));
-                w[i / 8][i % 8 / 2] = pack_bf16(p0, p1);
-                l += p0 + p1;
-            }
-            pf[u][0] = __builtin_bit_cast(bf16x8_t, w[0]);
-            pf[u][1] = __builtin_bit_cast(bf16x8_t, w[1]);
+            pf[u][0] = next[u][0];
+            pf[u][1] = next[u][1];
         }
+        tile_barrier();
     };
-    // Both groups' phases (the group as a constant: the compiler then knows what is on its way where).
-    const auto run = [&](auto group_number) __attribute__((always_inline)) {
-        constexpr int group = decltype(group_number)::value;
-        // phases A(it), B(it); k and v: the buffers of tile it, k1 and v1: of tile it + 1
-        const auto step = [&](int it, uint16_t *k, uint16_t *v, uint16_t *k1, uint16_t *v1)
-                              __attribute__((always_inline)) {
-            if constexpr (group == 0) send(it, k, v1);
-            phase_fence();
-            weigh(v);
-            scores(k1);
-            order_phase<SUB * 2 * DT, SUB * KS, AHEAD>();
-            phase_barrier<group == 1>();
-            if constexpr (group == 1) send(it + 1, k1, v);
-            weights(it + 1);
-            phase_barrier<group == 0>();
-        };
-        if constexpr (group == 1) phase_barrier<false>();
+
+    if (n_iter > 0) {
+        look_up(0);
+        locate(0, newest);
+        fetch(head_k, newest, k_col, sk0, L::kKeyBlock);
+        phase_fence();
+        look_up(tile_at(1));
+        send(-1, sk1, sv0);
+        // (every wave's keys 0 have landed; the rest has time until the first iteration)
+        phase_fence();
+        __builtin_amdgcn_s_waitcnt(wait_vm<2 * kLoads>());
+        __builtin_amdgcn_s_barrier();
+        phase_fence();
         scores(sk0);
-        phase_barrier<group == 1>();
-        if constexpr (group == 1) send(0, sk0, sv1);
-        weights(0);
-        phase_barrier<group == 0>();
+        bool rose;
+        raise(0, &rose);
+        weights(pf);
+        tile_barrier();
         int it = 0;
         if (n_iter > 2) {
             do {
@@ -485,26 +514,6 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
             ++it;
         }
         weigh(it & 1 ? sv1 : sv0);
-        // nothing of this wave's is on its way to LDS when it ends
-        __builtin_amdgcn_s_waitcnt(wait_vm<0>());
-        if constexpr (group == 0) phase_barrier<false>();  // (as many as group 1)
-    };
-
-    if (n_iter > 0) {
-        look_up(0);
-        locate(0, newest);
-        fetch(head_k, newest, k_col, sk0, L::kKeyBlock);
-        phase_fence();
-        look_up(tile_at(1));
-        send(-1, sk1, sv0);
-        // (every wave's keys 0 have landed; the rest has time until A(0))
-        phase_fence();
-        __builtin_amdgcn_s_waitcnt(wait_vm<2 * kLoads>());
-        phase_barrier<false>();
-        if (kGroups == 1 || wid < 4)
-            run(std::integral_constant<int, 0>{});
-        else
-            run(std::integral_constant<int, 1>{});
     }
 
     l += other_half(l);
@@ -575,21 +584,17 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int 
 }
 
 struct Plan {
-    int nw, splits;
+    int splits;
     int64_t tiles;  // at most this many tiles of rows: every sequence rounds up once
 };
-#ifndef SMALLF
-#define SMALLF 2
-#endif
 Plan plan_of(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
     const int64_t G = n_heads / c.n_kv, cus = device_cu_count();
     Plan p;
-    p.nw = (T * G / 256 + c.n_seqs) * c.n_kv < SMALLF * cus ? 4 : 8;
-    p.tiles = T * G / (32 * p.nw) + c.n_seqs;
+    p.tiles = T * G / kTileRows + c.n_seqs;
     const int64_t blocks = p.tiles * c.n_kv;
     int64_t keys = c.capacity;
-    if (window > 0 && int64_t(window) + sinks + 32 * p.nw < keys)
-        keys = int64_t(window) + sinks + 32 * p.nw;
+    if (window > 0 && int64_t(window) + sinks + kTileRows < keys)
+        keys = int64_t(window) + sinks + kTileRows;
     const int64_t key_tiles = (keys + 63) / 64;
     p.splits = 1;
     if (blocks < cus && key_tiles >= 8) {
@@ -599,26 +604,18 @@ Plan plan_of(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
     return p;
 }
 
-template <int DP, int NW, int KT>
-void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(p.tiles * c.n_kv * p.splits));
-    if (c.page_mask >= KT - 1)
-        hipLaunchKernelGGL((attn_prefill_kernel<DP, NW, KT, kTilePages>), grid, dim3(NW * 64), 0,
-                           stream, a, c, p.splits);
-    else if (c.page_mask >= 7)
-        hipLaunchKernelGGL((attn_prefill_kernel<DP, NW, KT, kSpanPages>), grid, dim3(NW * 64), 0,
-                           stream, a, c, p.splits);
-    else
-        hipLaunchKernelGGL((attn_prefill_kernel<DP, NW, KT, kAnyPages>), grid, dim3(NW * 64), 0,
-                           stream, a, c, p.splits);
-}
-
 template <int DP, int KT>
 void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t stream) {
-    if (p.nw == 8)
-        launch<DP, 8, KT>(p, a, c, stream);
+    const dim3 grid(static_cast<unsigned>(p.tiles * c.n_kv * p.splits)), block(kWaves * 64);
+    if (c.page_mask >= KT - 1)
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kTilePages>), grid, block, 0, stream, a, c,
+                           p.splits);
+    else if (c.page_mask >= 7)
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kSpanPages>), grid, block, 0, stream, a, c,
+                           p.splits);
     else
-        launch<DP, 4, KT>(p, a, c, stream);
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kAnyPages>), grid, block, 0, stream, a, c,
+                           p.splits);
 }
 
 }  // namespace
