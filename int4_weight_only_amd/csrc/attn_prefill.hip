@@ -16,7 +16,7 @@
 // The running maximum M (in units of log2) is only raised when a tile exceeds it by more than 2^8:
 // the weights then stay below 2^8 and keep their relative precision, and the accumulators are
 // rarely rescaled.
-#include <type_traits>
+#include <algorithm>
 
 #include "attn_device.h"
 
@@ -26,18 +26,6 @@ namespace {
 
 constexpr int kWaves = 4, kTileRows = 32 * kWaves;
 constexpr int kSlack = 8;
-#ifndef VG
-#define VG 0
-#endif
-#ifndef OVER
-#define OVER 1
-#endif
-#ifndef AHEADV
-#define AHEADV 3
-#endif
-#ifndef AHEAD
-#define AHEAD 4
-#endif
 
 // A block's rows: of sequence `seq`, stacked rows row0 .. row0 + BM - 1 of `rows`; token row q0 and
 // position pos0 of stacked row 0.
@@ -108,19 +96,18 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
     return false;
 }
 
-// Orders a run of N products, each with READS LDS reads for its fragment, every fragment read
-// NAHEAD products before its use, and VECTOR vector instructions after each product. (Left to itself
-// the scheduler keeps two fragments in flight, where a product waits for most of an LDS read, and
-// computes the weights before the products.)
-template <int N, int READS, int NAHEAD, int VECTOR>
+// Orders a run of N products, each with READS LDS reads for its fragment, every fragment read AHEAD
+// products before its use. (Left to itself the scheduler keeps two fragments in flight, where a
+// product waits for most of an LDS read. At 256 dims registers are short: 4 key fragments ahead
+// instead of 2 cost 10 %.)
+template <int N, int READS, int AHEAD>
 __device__ __forceinline__ void order_products() {
-    constexpr int kVector = 0x002, kMatrix = 0x008, kLdsRead = 0x100;
-    __builtin_amdgcn_sched_group_barrier(kLdsRead, READS * NAHEAD, 0);
+    constexpr int kMatrix = 0x008, kLdsRead = 0x100;
+    __builtin_amdgcn_sched_group_barrier(kLdsRead, READS * AHEAD, 0);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         __builtin_amdgcn_sched_group_barrier(kMatrix, 1, 0);
-        if (i + NAHEAD < N) __builtin_amdgcn_sched_group_barrier(kLdsRead, READS, 0);
-        if constexpr (VECTOR > 0) __builtin_amdgcn_sched_group_barrier(kVector, VECTOR, 0);
+        if (i + AHEAD < N) __builtin_amdgcn_sched_group_barrier(kLdsRead, READS, 0);
     }
 }
 
@@ -356,10 +343,10 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         look_up(tile_at(it + 3));
     };
 
-    // An iteration multiplies the keys of tile i + 1, then the values of tile i while the scores of
-    // tile i + 1 become weights (vector instructions between the products), so that the matrix cores
-    // work through the softmax. send(i) overwrites the buffers of keys i and values i - 1, read in the
-    // iteration before, and has the iteration to land: one barrier a tile.
+    // An iteration multiplies the keys of tile i + 1 and the values of tile i, then turns the scores
+    // of tile i + 1 into weights, while the other workgroup of the compute unit multiplies. send(i)
+    // overwrites the buffers of keys i and values i - 1, read in the iteration before, and has the
+    // iteration to land: one barrier a tile.
     floatx16_t s[SUB];
     bf16x8_t pf[SUB][2];  // the weights of the tile whose values come next
 
@@ -438,7 +425,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         }
         return f;
     };
-    const auto weights = [&](bf16x8_t (&w)[SUB][2]) __attribute__((always_inline)) {
+    const auto weights = [&]() __attribute__((always_inline)) {
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
             uintx4_t x[2];
@@ -449,8 +436,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
                 l += p0 + p1;
                 x[i / 8][i % 8 / 2] = pack_bf16(p0, p1);
             }
-            w[u][0] = __builtin_bit_cast(bf16x8_t, x[0]);
-            w[u][1] = __builtin_bit_cast(bf16x8_t, x[1]);
+            pf[u][0] = __builtin_bit_cast(bf16x8_t, x[0]);
+            pf[u][1] = __builtin_bit_cast(bf16x8_t, x[1]);
         }
     };
 
@@ -459,28 +446,17 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
                           __attribute__((always_inline)) {
         send(it, k, v1);
         scores(k1);
-        order_products<SUB * KS, 1, AHEAD, 0>();
+        order_products<SUB * KS, 1, (DP > 128 ? 2 : 4)>();
         bool rose;
         const float f = raise(it + 1, &rose);
-        // (at 256 dims the registers do not hold both tiles' weights: the softmax after the products)
-        constexpr bool kOver = DP <= 128 && OVER;
-        bf16x8_t next[SUB][2];
         weigh(v);
-        if constexpr (kOver) weights(next);
-        order_products<SUB * 2 * DT, 2, AHEADV, kOver ? VG : 0>();
-        if constexpr (!kOver) {
-            phase_fence();
-            weights(next);
-        }
+        order_products<SUB * 2 * DT, 2, 3>();
+        phase_fence();
         if (rose) {
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[d] *= f;
         }
-#pragma unroll
-        for (int u = 0; u < SUB; ++u) {
-            pf[u][0] = next[u][0];
-            pf[u][1] = next[u][1];
-        }
+        weights();
         tile_barrier();
     };
 
@@ -499,7 +475,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         scores(sk0);
         bool rose;
         raise(0, &rose);
-        weights(pf);
+        weights();
         tile_barrier();
         int it = 0;
         if (n_iter > 2) {
@@ -554,7 +530,9 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         }
 }
 
-// Joins the splits of a (token row, head), one wave each, in order.
+// Joins the splits of a (token row, head), one wave each: groups of LANES lanes, 4 dims a lane, take
+// every (64 / LANES)th split and meet at the end, all in a fixed order.
+template <int LANES>
 __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int D, int n_seqs,
                                                                 int splits) {
     const int64_t pairs = a.T * a.n_heads;
@@ -563,19 +541,32 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int 
     const int64_t token = pair / a.n_heads;
     // (rows that q_start gives to no sequence have no partial results)
     if (pair >= pairs || token < a.q_start[0] || token >= a.q_start[n_seqs]) return;
-    const int col = 4 * lane;
+    const int col = 4 * (lane % LANES), at = min(col, D - 4);
     float m = kNoMax, l = 0.0f;
     floatx4_t v = floatx4_t(0.0f);
-    for (int i = 0; i < splits; ++i) {
-        const Partials p = partials(a.work, pairs, splits, i, D);
-        const float m1 = p.ml[2 * pair], l1 = p.ml[2 * pair + 1];
-        if (l1 == 0.0f) continue;
+    const auto add = [&](float m1, float l1, floatx4_t v1) {
         const float m2 = fmaxf(m, m1);
         const float f = __builtin_amdgcn_exp2f(m - m2), f1 = __builtin_amdgcn_exp2f(m1 - m2);
         m = m2;
         l = l * f + l1 * f1;
-        if (col < D) v = v * f + f1 * *reinterpret_cast<const floatx4_t *>(p.o + pair * D + col);
+        v = v * f + v1 * f1;
+    };
+#pragma unroll 4
+    for (int i = lane / LANES; i < splits; i += kWave / LANES) {
+        const Partials p = partials(a.work, pairs, splits, i, D);
+        const float m1 = p.ml[2 * pair], l1 = p.ml[2 * pair + 1];
+        const floatx4_t v1 = *reinterpret_cast<const floatx4_t *>(p.o + pair * D + at);
+        // (a split without keys has written no weighted sums)
+        add(m1, l1, l1 > 0.0f ? v1 : floatx4_t(0.0f));
     }
+#pragma unroll
+    for (int o = LANES; o < kWave; o <<= 1) {
+        floatx4_t v1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v1[i] = __shfl_xor(v[i], o, kWave);
+        add(__shfl_xor(m, o, kWave), __shfl_xor(l, o, kWave), v1);
+    }
+    if (lane >= LANES) return;
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
     if (a.lse && lane == 0) a.lse[pair] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
     if (col < D)
@@ -597,10 +588,11 @@ Plan plan_of(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
         keys = int64_t(window) + sinks + kTileRows;
     const int64_t key_tiles = (keys + 63) / 64;
     p.splits = 1;
-    if (blocks < cus && key_tiles >= 8) {
-        const int64_t most = key_tiles / 4 < 64 ? key_tiles / 4 : 64;
-        p.splits = static_cast<int>(2 * cus / blocks < most ? 2 * cus / blocks : most);
-    }
+    // Few rows over many keys: the keys split over workgroups, four tiles each at least. (28 / 4 heads
+    // of 128: 16 tokens of 2 sequences after 16000 keys 457 us unsplit, 30 split; at least 2 or 8 tiles
+    // each: 16 tokens after 2000 keys 22 and 19 us for 15.)
+    if (blocks < cus && key_tiles >= 8)
+        p.splits = static_cast<int>(std::min({2 * cus / blocks, key_tiles / 4, int64_t{64}}));
     return p;
 }
 
@@ -637,9 +629,11 @@ hipError_t launch_attn_prefill(const AttnArgs &a, const KvView &c, hipStream_t s
     if (p.splits > 1) {
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
-        const int64_t pairs = a.T * a.n_heads;
-        hipLaunchKernelGGL(attn_prefill_join_kernel, dim3(static_cast<unsigned>((pairs + 3) / 4)),
-                           dim3(256), 0, stream, a, c.head_dim, c.n_seqs, p.splits);
+        const dim3 grid(static_cast<unsigned>((a.T * a.n_heads + 3) / 4)), block(256);
+        const auto join = c.head_dim <= 64    ? attn_prefill_join_kernel<16>
+                          : c.head_dim <= 128 ? attn_prefill_join_kernel<32>
+                                              : attn_prefill_join_kernel<64>;
+        hipLaunchKernelGGL(join, grid, block, 0, stream, a, c.head_dim, c.n_seqs, p.splits);
     }
     return hipGetLastError();
 }
