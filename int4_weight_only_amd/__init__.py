@@ -133,14 +133,20 @@ def _check(fn, status):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    """The current stream of a device, as an address (without a torch.cuda.Stream object, whose
+    making costs a small call a tenth of its time)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _need(t, name, dtype, device=None, dim=None):
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda
+            and (device is None or t.device == device) and (dim is None or t.ndim == dim)
+            and (t.ndim == 0 or t.stride(-1) == 1)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -521,22 +527,37 @@ def w4_rope_frequencies(rot_dim, scaling=W4_ROPE_PLAIN, base=10000.0, factor=1.0
 def _kv_cache(k_cache, v_cache, page_table, kv_len, dev):
     """The ABI's view of a cache [n_pages][page_size][n_kv_heads][head_dim] (any strides with the
     last dim contiguous; another order of slots and heads is a permuted view)."""
-    _need(k_cache, "k_cache", torch.bfloat16, dev, 4)
-    _need(v_cache, "v_cache", torch.bfloat16, dev, 4)
-    _need(page_table, "page_table", torch.int32, dev, 2)
-    _need(kv_len, "kv_len", torch.int32, dev, 1)
-    n_pages, page_size, n_kv, D = k_cache.shape
-    # the stride of a dimension of one element says nothing
-    sp, ss, sh, _ = (s if n > 1 else 0 for n, s in zip(k_cache.shape, k_cache.stride()))
-    if v_cache.shape != k_cache.shape or any(
-            n > 1 and s != t for n, s, t in zip(k_cache.shape, k_cache.stride(), v_cache.stride())):
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
-    n_seqs, cols = page_table.shape
-    if kv_len.shape[0] != n_seqs:
+    if not (k_cache.dtype is v_cache.dtype is torch.bfloat16
+            and page_table.dtype is kv_len.dtype is torch.int32
+            and k_cache.device == v_cache.device == page_table.device == kv_len.device == dev
+            and k_cache.is_cuda):
+        _need(k_cache, "k_cache", torch.bfloat16, dev)
+        _need(v_cache, "v_cache", torch.bfloat16, dev)
+        _need(page_table, "page_table", torch.int32, dev)
+        _need(kv_len, "kv_len", torch.int32, dev)
+    try:
+        n_pages, page_size, n_kv, D = shape = k_cache.shape
+        n_seqs, cols = page_table.shape
+        n_lens, = kv_len.shape
+    except ValueError:
+        raise ValueError("k_cache and v_cache must have 4 dims, page_table 2 and kv_len 1") from None
+    sp, ss, sh, sd = strides = k_cache.stride()
+    if v_cache.shape != shape or v_cache.stride() != strides or n_pages == 1 or page_size == 1 \
+            or n_kv == 1:
+        # the stride of a dimension of one element says nothing
+        if v_cache.shape != shape or any(n > 1 and x != y for n, x, y in
+                                         zip(shape, strides, v_cache.stride())):
+            raise ValueError("k_cache and v_cache must have the same shape and strides")
+        sp, ss, sh = (x if n > 1 else 0 for n, x in zip(shape, strides[:3]))
+    ld, one = page_table.stride()
+    if (sd != 1 and D > 1) or (one != 1 and cols > 1) or (n_lens > 1 and kv_len.stride(0) != 1):
+        raise ValueError("k_cache, v_cache, page_table and kv_len must be contiguous along their "
+                         "last dim")
+    if n_lens != n_seqs:
         raise ValueError(f"kv_len must have {n_seqs} elements")
     return _KvCache(k_cache.data_ptr(), v_cache.data_ptr(), n_pages, sp, ss, sh, page_size, n_kv,
-                    D, page_table.data_ptr(), n_seqs, cols,
-                    page_table.stride(0) if n_seqs > 1 else cols, kv_len.data_ptr())
+                    D, page_table.data_ptr(), n_seqs, cols, ld if n_seqs > 1 else cols,
+                    kv_len.data_ptr())
 
 
 def _need_q_start(q_start, n_seqs, dev):
