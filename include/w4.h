@@ -427,6 +427,8 @@ int w4_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int n_heads,
  *          w4_gemv_ws; may be NULL when that size is 0
  * Long caches are split over several compute units and joined in order (deterministic).
  * w4_attn_decode_work_bytes reads only sizes, no array; 0 for arguments the call rejects.
+ * Limits (W4_ERR_RANGE beyond them): n_seqs * n_heads < 2^31, and n_seqs * n_heads times the
+ * number of 32-key tiles that table_cols pages can hold < 2^31.
  */
 int w4_attn_decode(const uint16_t *q, int64_t ldq, int n_heads, const w4_kv_cache *cache,
                    float scale, int64_t window, int64_t sinks, void *y, int64_t ldy,
@@ -439,8 +441,8 @@ size_t w4_attn_decode_work_bytes(int n_heads, const w4_kv_cache *cache, int64_t 
  * each at its own position: prompts, chunks of prompts, or several new tokens per sequence.
  *   q      bf16 [T][ldq];  q_start int32 [n_seqs + 1];  y [T][ldy];  lse fp32 [T][n_heads] or NULL
  *   the other arguments as for w4_attn_decode.
- * T * n_heads and n_seqs * n_heads must be below 2^31 (W4_ERR_RANGE; n_seqs * n_heads also for
- * w4_attn_decode).  The softmax weights enter the second product as bf16, their sum in fp32.
+ * Limits: T * n_heads and n_seqs * n_heads below 2^31 (W4_ERR_RANGE).  The softmax weights enter
+ * the second product as bf16, their sum in fp32.
  */
 int w4_attn_prefill(const uint16_t *q, int64_t T, int64_t ldq, int n_heads,
                     const int32_t *q_start, const w4_kv_cache *cache, float scale,

@@ -13,11 +13,16 @@
 //
 // A sequence's visible keys (its sinks, then its window; all without a window) are cut into tiles
 // of 32 keys. Every unit (sequence, key-value head, 16 query heads) is cut into equal shares of at
-// most `per` tiles, a workgroup each, `per` being such that the shares of all sequences together fill
-// the card once: ragged lengths leave no compute unit idle. In a workgroup each of the four waves
-// takes every fourth tile on its own (no barrier in the loop, the next tile's loads in flight), and
-// the waves join in LDS. The shares of a unit that was cut meet in the caller's workspace, and a
-// second kernel joins them in order.
+// most `per` tiles, a workgroup each, `per` being such that the shares of all sequences together
+// fill the card once: ragged lengths leave no compute unit idle. In a workgroup each of the four
+// waves takes every fourth tile on its own (no barrier in the loop, the next tile's loads in
+// flight), and the waves join in LDS. The shares of a unit that was cut meet in the caller's
+// workspace, and a second kernel joins them in order.
+//
+// 28 heads over 4 of 128: 4 sequences of up to 131072 keys 188 us (5.5 TB/s of keys and values,
+// more than a large copy's 4.9), 32 of up to 8192 64 us (4.3 TB/s). One sequence of 4097 keys takes
+// 11 us: nothing but waits for memory, one after the other (page, keys, partial results), and two
+// launches.
 #include <type_traits>
 
 #include "attn_device.h"
@@ -138,7 +143,9 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
     constexpr int kChunks = DP / 8;  // 16-byte chunks of a row
     constexpr int kVRows = 64 / kChunks;       // rows a wave's load instruction covers
     constexpr int kVLoads = kTile / kVRows;
-    constexpr int kRow = Rows<DP>::kValue;
+    // elements from row to row of a value tile: a transposed read takes 32 bytes of 4 consecutive
+    // rows at once, which the gap puts 32 bytes further each in the 64 banks
+    constexpr int kRow = DP + 16;
     // per wave: the value tile, 32 rows of bf16; after the loop its sums, 16 rows of fp32
     __shared__ __attribute__((aligned(16))) uint16_t sv[kWaves][kTile * kRow];
     __shared__ float sm[kWaves][kRows], sl[kWaves][kRows];
@@ -190,7 +197,8 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
 
         bf16x8_t qf[KS];
         {
-            const uint16_t *src = a.q + b * a.ldq + static_cast<int64_t>(head0 + min(r, n_rows - 1)) * D;
+            const uint16_t *src =
+                a.q + b * a.ldq + static_cast<int64_t>(head0 + min(r, n_rows - 1)) * D;
 #pragma unroll
             for (int s = 0; s < KS; ++s) {
                 const int d = 32 * s + 8 * g;
@@ -204,9 +212,9 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
         const auto visible = [&](int p) {
             return (p <= keys.last) & ((p >= keys.lo) | (p < a.sinks));
         };
-        // 16 keys as they are read: the page offset of a visible key among them (of the newest key if
-        // there is none), and that key. Keys that are not visible are read from it: finite values,
-        // whose weight is 0.
+        // 16 keys as they are read: the page offset of a visible key among them (of the newest key
+        // if there is none), and that key. Keys that are not visible are read from it: finite
+        // values, whose weight is 0.
         struct Span {
             int start, safe;
             int64_t page;
@@ -231,8 +239,8 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
                 reinterpret_cast<const char *>(kv + page) + 2u * off);
         };
 
-        // The next tile to be fetched, and the one after it: their spans' keys, and the table entries
-        // on their way.
+        // The next tile to be fetched, and the one after it: their spans' keys, and the table
+        // entries on their way.
         Span next[2];
         int entry[2] = {0, 0};
         const auto look_up = [&](int t) {
@@ -249,7 +257,8 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
                 next[u].page = page_offset(entry[u]);
             }
         };
-        // Dims past D repeat the row's last chunk: they meet zeros of q, or outputs that are not kept.
+        // Dims past D repeat the row's last chunk: they meet zeros of q, or outputs that are not
+        // kept.
         const int v_row = lane / kChunks, v_chunk = min(8 * (lane % kChunks), D - 8);
         uintx4_t rk[2][KS], rv[kVLoads];
         const auto fetch_k = [&] {
@@ -479,10 +488,11 @@ Plan plan_of(int n_heads, const KvView &c, int window, int sinks) {
     // sequences (a unit for every compute unit) of 1000 keys 28 / 35, of 2000 50 / 58.
     p.whole_units = tiles <= (p.units >= cus ? 64 : 16);
     // Workgroups that run at once (by registers; 6 at 64 dims measured better than the 4 that fit:
-    // 64 x 3000 keys, 8 heads, 76 us for 85). Few units: shares that fill the card once, where every
-    // unit rounds up by half a share. Many: about two rounds, which even out by themselves. (32 ragged
-    // sequences of up to 8192 keys, 128 units, us at 1 / 2 / 3 / 4 times the compute units: 78 / 73 /
-    // 65 / 64; 100 of up to 6000, 400 units: 164 / 144 / 144 / 144, at 6 times 141.)
+    // 64 x 3000 keys, 8 heads, 76 us for 85). Few units: shares that fill the card once, where
+    // every unit rounds up by half a share. Many: about two rounds, which even out by themselves.
+    // (32 ragged sequences of up to 8192 keys, 128 units, us at 1 / 2 / 3 / 4 times the compute
+    // units: 78 / 73 / 65 / 64; 100 of up to 6000, 400 units: 164 / 144 / 144 / 144, at 6 times
+    // 141.)
     const int resident = cus * (c.head_dim > 128 ? 1 : c.head_dim > 64 ? 3 : 6);
     p.aim = p.units <= resident / 2 ? resident - p.units / 2 : 2 * resident;
     const int64_t most = p.units * ((tiles + kWaves - 1) / kWaves);  // shares of kWaves tiles

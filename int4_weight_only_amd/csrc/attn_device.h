@@ -1,5 +1,5 @@
-// attn_device.h -- pieces shared by the attention kernels: matrix-core types, the layout of key
-// and value tiles in LDS, the join of partial results.
+// attn_device.h -- pieces shared by the attention kernels: matrix-core types, transposed LDS
+// reads, output stores, sums and maxima over lanes.
 #pragma once
 
 #include "w4_device.h"
@@ -34,15 +34,6 @@ __device__ __forceinline__ uintx2_t lds_read_transposed(const uint16_t *p) {
     return __builtin_bit_cast(uintx2_t,
                               __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p)));
 }
-
-// Rows of a tile in LDS are DP elements and a gap, against bank conflicts (64 banks of 4 bytes), with
-// every access at a constant offset from one address per lane:
-//   keys:   a fragment reads the same 16 bytes of 16 or 32 consecutive rows: 16 bytes further each
-//   values: a transposed read takes 32 bytes of 4 consecutive rows at once: 32 bytes further each
-template <int DP>
-struct Rows {
-    static constexpr int kKey = DP + 8, kValue = DP + 16;  // elements from row to row
-};
 
 // Four consecutive elements of an output row, from element idx (a multiple of 4) on. `wide`: the
 // output's base and rows allow one store.

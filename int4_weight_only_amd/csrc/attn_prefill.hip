@@ -15,7 +15,16 @@
 //
 // The running maximum M (in units of log2) is only raised when a tile exceeds it by more than 2^8:
 // the weights then stay below 2^8 and keep their relative precision, and the accumulators are
-// rarely rescaled.
+// rarely rescaled. The weights enter the second product as bf16 (each within 2^-8 of itself, like
+// the keys and values; a second product for what is cut off, as the decode kernel has it, would
+// cost half as much again); their sum takes them before that rounding.
+//
+// A workgroup is four waves, 128 stacked rows; tiles of 64 keys (32 at 256 dims) go from memory
+// straight to LDS, double buffered, one barrier a tile. Two workgroups run on a compute unit, so
+// that one multiplies while the other turns scores into weights. Bound by instruction issue:
+// exponentials, maxima, sums and packing take about as long as the products, and overlap with them
+// in part. Three prompts of about 4096 tokens, 28 heads over 4 of 128: 305 us, 940 TFLOP/s of the
+// 1350 that a large matrix product reaches here; the matrix cores are busy half of the time.
 #include <algorithm>
 
 #include "attn_device.h"
@@ -34,9 +43,9 @@ struct Tile {
 };
 
 // Tiles of BM rows of all sequences in the order in which they are given out: the tiles that see
-// most keys first (by their level: the tile's number in its sequence plus the tiles its earlier keys
-// would make), so that the last ones to run are short. Up to 64 sequences, a lane each; more are
-// taken in order, the last rows of each first. Every lane of every wave takes part.
+// most keys first (by their level: the tile's number in its sequence plus the tiles its earlier
+// keys would make), so that the last ones to run are short. Up to 64 sequences, a lane each; more
+// are taken in order, the last rows of each first. Every lane of every wave takes part.
 template <int BM>
 __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_start, int64_t T,
                                           int G, int tile, Tile *out) {
@@ -59,8 +68,8 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
         }
         int w, row_tile;  // the lane of the sequence, the tile's number in it
         if (c.n_seqs <= kWave) {
-            // levels first .. first + mine - 1 are this sequence's; the largest level with more than
-            // `tile` tiles at it or above
+            // levels first .. first + mine - 1 are this sequence's; the largest level with more
+            // than `tile` tiles at it or above
             const int first = static_cast<int>(
                 min(static_cast<int64_t>(max(n_keys - nq, 0)) * G / BM, int64_t{1} << 29));
             int lo = 0, hi = wave_max_dpp(first + mine);
@@ -137,10 +146,10 @@ __device__ __forceinline__ Partials partials(void *work, int64_t pairs, int spli
 }
 
 // A tile in LDS: direct loads from memory, which lay 64 lanes of 16 bytes down in a row, put kSpan
-// consecutive rows of DP elements into a block of 1 KiB; blocks follow each other with a gap. Inside
-// a row the 16-byte chunks are permuted (by the choice of what each lane loads), so that neither the
-// key fragments (one chunk of 16 or 32 consecutive rows) nor the transposed value reads (32 bytes of
-// 4 consecutive rows) meet in the same of the 64 banks: chunk c of row r is at place
+// consecutive rows of DP elements into a block of 1 KiB; blocks follow each other with a gap.
+// Inside a row the 16-byte chunks are permuted (by the choice of what each lane loads), so that
+// neither the key fragments (one chunk of 16 or 32 consecutive rows) nor the transposed value reads
+// (32 bytes of 4 consecutive rows) meet in the same of the 64 banks: chunk c of row r is at place
 //   c ^ key_swap(r) for keys,   c ^ 4 value_swap(r) for values,
 // rows of 128, 256 and 512 bytes covering 1/2, 1 and 2 rows of banks.
 template <int DP>
@@ -149,7 +158,9 @@ struct TileLayout {
     static constexpr int kKeyBlock = 512 + (DP > 128 ? 16 : 32);   // elements from block to block
     static constexpr int kValueBlock = 512 + (DP > 128 ? 64 : 0);
     static constexpr int kValueSwaps = DP == 128 ? 4 : 2;  // values that value_swap takes
-    __device__ static int key_swap(int r) { return DP > 128 ? r & 1 : DP > 64 ? r & 3 : r >> 1 & 3; }
+    __device__ static int key_swap(int r) {
+        return DP > 128 ? r & 1 : DP > 64 ? r & 3 : r >> 1 & 3;
+    }
     __device__ static int value_swap(int r) {
         return DP > 128 ? r & 1 : DP > 64 ? r & 3 : r >> 1 & 1;
     }
@@ -244,10 +255,10 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
     const int before = a.window > 0 ? pos - a.window : -1;  // newest position out of the window
     float M = kNoMax, l = 0.0f;
 
-    // Staging: in each of kLoads instructions a wave moves kSpan consecutive rows of the tile. A row
-    // whose key no row of the block sees is read from one that some row sees (finite; its weights are
-    // 0; of the same rows, if there is any); dims past D from the row's last chunk (they meet zeros of
-    // q, or outputs that are not kept).
+    // Staging: in each of kLoads instructions a wave moves kSpan consecutive rows of the tile. A
+    // row whose key no row of the block sees is read from one that some row sees (finite; its
+    // weights are 0; of the same rows, if there is any); dims past D from the row's last chunk
+    // (they meet zeros of q, or outputs that are not kept).
     const int my_row = lane / kChunks;
     const int k_col = min(8 * (lane % kChunks ^ L::key_swap(my_row)), D - 8);
     const int v_col = min(8 * (lane % kChunks ^ 4 * L::value_swap(my_row)), D - 8);
@@ -261,7 +272,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
     const auto visible = [&](int p) {
         return (p <= tile_last) & ((p >= lo) | (p < sinks_end));
     };
-    const auto safe_of = [&](int s0, int n) {  // a key that is seen, among the n from s0 on if any is
+    // a key that is seen, among the n from s0 on if any is
+    const auto safe_of = [&](int s0, int n) {
         if (s0 > tile_last) return tile_last;
         if (s0 < sinks_end) return s0;
         return s0 + n - 1 < lo ? lo : max(s0, lo);
@@ -283,7 +295,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
     const auto look_up = [&](int it) {  // the page table entries of a tile
         const int k0 = tile_key(it);
         if constexpr (PAGES == kTilePages) {
-            entry[0] = read_const(table + (k0 >> c.page_shift));  // (its first key or a later one is seen)
+            // (the page of the tile's first key, which is seen or a later one is)
+            entry[0] = read_const(table + (k0 >> c.page_shift));
         } else if constexpr (PAGES == kSpanPages) {
             const bool all = all_seen(k0);
 #pragma unroll
@@ -332,8 +345,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
                             2u * (w.off[i] + col),
                         dst + (i * NW + wid) * block);
     };
-    // Sends for the keys of tile it + 2 and the values of tile it + 1, whose rows were found for its
-    // keys. (Past the last tile both repeat it, into buffers that nothing reads any more.)
+    // Sends for the keys of tile it + 2 and the values of tile it + 1, whose rows were found for
+    // its keys. (Past the last tile both repeat it, into buffers that nothing reads any more.)
     Where newest;  // of tile it + 1
     const auto tile_at = [&](int it) { return min(it, n_iter - 1); };
     const auto send = [&](int it, uint16_t *k, uint16_t *v) __attribute__((always_inline)) {
@@ -343,16 +356,17 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         look_up(tile_at(it + 3));
     };
 
-    // An iteration multiplies the keys of tile i + 1 and the values of tile i, then turns the scores
-    // of tile i + 1 into weights, while the other workgroup of the compute unit multiplies. send(i)
-    // overwrites the buffers of keys i and values i - 1, read in the iteration before, and has the
-    // iteration to land: one barrier a tile.
+    // An iteration multiplies the keys of tile i + 1 and the values of tile i, then turns the
+    // scores of tile i + 1 into weights, while the other workgroup of the compute unit multiplies.
+    // send(i) overwrites the buffers of keys i and values i - 1, read in the iteration before, and
+    // has the iteration to land: one barrier a tile.
     floatx16_t s[SUB];
     bf16x8_t pf[SUB][2];  // the weights of the tile whose values come next
 
     const auto scores = [&](const uint16_t *k) __attribute__((always_inline)) {
         // (chunks 2 ks + half, swapped: even and odd steps each at constant offsets)
-        const uint16_t *kp[2] = {k + L::key_at(lane & 31, half), k + L::key_at(lane & 31, 2 + half)};
+        const uint16_t *kp[2] = {k + L::key_at(lane & 31, half),
+                                 k + L::key_at(lane & 31, 2 + half)};
 #pragma unroll
         for (int u = 0; u < SUB; ++u) s[u] = floatx16_t(0.0f);
 #pragma unroll
@@ -389,8 +403,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
                         __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);
                 }
     };
-    // Hides the scores of the keys that a row does not see, and raises M; returns the factor that the
-    // sums so far have to take if it rose for any row (`rose`).
+    // Hides the scores of the keys that a row does not see, and raises M; returns the factor that
+    // the sums so far have to take if it rose for any row (`rose`).
     const auto raise = [&](int it, bool *rose) __attribute__((always_inline)) {
         const int k0 = tile_key(it);
         // every key of the tile seen by every row of the wave?
@@ -399,7 +413,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         if (!whole) {
             // key i of the lane's is at place 32 u + 8 (i / 4) + i % 4 of those from k0 + 4 half on
             const int base = k0 + 4 * half;
-            const int newest_at = pos - base, before_at = before - base, sinks_at = sinks_end - base;
+            const int newest_at = pos - base, before_at = before - base;
+            const int sinks_at = sinks_end - base;
 #pragma unroll
             for (int u = 0; u < SUB; ++u)
 #pragma unroll
@@ -530,8 +545,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         }
 }
 
-// Joins the splits of a (token row, head), one wave each: groups of LANES lanes, 4 dims a lane, take
-// every (64 / LANES)th split and meet at the end, all in a fixed order.
+// Joins the splits of a (token row, head), one wave each: groups of LANES lanes, 4 dims a lane,
+// take every (64 / LANES)th split and meet at the end, all in a fixed order.
 template <int LANES>
 __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int D, int n_seqs,
                                                                 int splits) {
@@ -588,9 +603,9 @@ Plan plan_of(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
         keys = int64_t(window) + sinks + kTileRows;
     const int64_t key_tiles = (keys + 63) / 64;
     p.splits = 1;
-    // Few rows over many keys: the keys split over workgroups, four tiles each at least. (28 / 4 heads
-    // of 128: 16 tokens of 2 sequences after 16000 keys 457 us unsplit, 30 split; at least 2 or 8 tiles
-    // each: 16 tokens after 2000 keys 22 and 19 us for 15.)
+    // Few rows over many keys: the keys split over workgroups, four tiles each at least. (28 / 4
+    // heads of 128: 16 tokens of 2 sequences after 16000 keys 457 us unsplit, 30 split; at least 2
+    // or 8 tiles each: 16 tokens after 2000 keys 22 and 19 us for 15.)
     if (blocks < cus && key_tiles >= 8)
         p.splits = static_cast<int>(std::min({2 * cus / blocks, key_tiles / 4, int64_t{64}}));
     return p;

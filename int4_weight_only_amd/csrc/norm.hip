@@ -152,10 +152,10 @@ void launch_nt(const NormArgs &a, hipStream_t stream) {
                        a);
 }
 
-// One chunk of 8 elements a thread, as far as 512 threads go: what a thread holds it also waits for.
-// (8192 rows of 3584, fp32 residual: 64 threads of 8 chunks 93 us, 128 of 4 83, 256 of 2 73, 512 of
-// 1 69; 3000 rows of 8192, bf16: 256 of 4 46, 512 of 2 41, 1024 of 1 43; 1700 of 16384: 256 of 8 89,
-// 512 of 4 57, 1024 of 2 46.)
+// One chunk of 8 elements a thread, as far as 512 threads go: what a thread holds it also waits
+// for. (8192 rows of 3584, fp32 residual: 64 threads of 8 chunks 93 us, 128 of 4 83, 256 of 2 73,
+// 512 of 1 69; 3000 rows of 8192, bf16: 256 of 4 46, 512 of 2 41, 1024 of 1 43; 1700 of 16384: 256
+// of 8 89, 512 of 4 57, 1024 of 2 46.)
 template <typename R>
 void launch_r(const NormArgs &a, hipStream_t stream) {
     const int64_t chunks = (a.d + 7) / 8;
