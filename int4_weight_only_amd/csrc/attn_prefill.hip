@@ -23,7 +23,7 @@
 // straight to LDS, double buffered, one barrier a tile. Two workgroups run on a compute unit, so
 // that one multiplies while the other turns scores into weights. Bound by instruction issue:
 // exponentials, maxima, sums and packing take about as long as the products, and overlap with them
-// in part. Three prompts of about 4096 tokens, 28 heads over 4 of 128: 305 us, 940 TFLOP/s of the
+// in part. Three prompts of up to 4096 tokens, 28 heads over 4 of 128: 296 us, 968 TFLOP/s of the
 // 1350 that a large matrix product reaches here; the matrix cores are busy half of the time.
 #include <algorithm>
 
