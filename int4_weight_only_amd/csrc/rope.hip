@@ -7,7 +7,7 @@
 // bf16, at position 10^5.
 //
 // Memory-bound: qkv is read once, q and the new cache rows are written once. 8 prompts of up to
-// 2048 tokens, 28 + 4 + 4 heads of 128: 239 MB in 46 us, 5.2 TB/s, a large copy's rate. One token:
+// 2048 tokens, 28 + 4 + 4 heads of 128: 239 MB in 41 to 46 us, a large copy's rate or more. One token:
 // 4 us, the launch and two waits for memory (length and page, then the row).
 #include "w4_device.h"
 #include "w4_launch.h"
@@ -28,7 +28,9 @@ __device__ __forceinline__ void turn(int pos, float inv_freq, float factor, floa
 // every query and key head; the heads' values move in 16-byte pieces: `u` rotated pieces of a head
 // (LAYOUT half: 8 pairs, read and written as two pieces R / 2 apart; interleaved: 4 pairs, one
 // piece), then the pieces past R and the value heads, copied. ANY: heads whose R does not fall on
-// those pieces (R % 16 for the half layout, R % 8 for the interleaved), element by element.
+// those pieces (R % 16 for the half layout, R % 8 for the interleaved), see rotate_any. (8 prompts
+// of up to 2048 tokens, 32 + 8 + 8 heads of 96: R = 32 57 us, halves of 12 71, 36 interleaved 57;
+// element by element 90 and 94.)
 enum { kHalf = 0, kInterleaved = 1, kAny = 2 };
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;
@@ -48,6 +50,49 @@ __device__ __forceinline__ void pack8(uint16_t *p, const float *v) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
     *reinterpret_cast<uintx4_t *>(p) = w;
+}
+
+// Elements d .. d + 7 of a head at any even R. The half layout's partners stand R / 2 before or
+// after: 16 bytes at any alignment, of both sides where the eight lie in both halves. Those of the
+// second half may pass the head's end, into the value heads that follow; those of the first may
+// begin before it: `lead`, the row has elements before this head, else they are read one by one.
+__device__ __forceinline__ void rotate_any(const uint16_t *src, uint16_t *dst, int d, int R,
+                                           int interleaved, bool lead, const float *cosine,
+                                           const float *sine) {
+    typedef uint32_t uintx4_any_t __attribute__((ext_vector_type(4), aligned(2), may_alias));
+    const uintx4_t own = *reinterpret_cast<const uintx4_t *>(src + d);
+    const int half = R / 2;
+    uint32_t x[8], other[8], out[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = own[i / 2] >> 16 * (i % 2) & 0xFFFFu;
+    if (interleaved) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) other[i] = x[i ^ 1];
+    } else {
+        uintx4_t after = own, before = own;
+        if (d < half) after = *reinterpret_cast<const uintx4_any_t *>(src + d + half);
+        if (d >= half || (d + 8 > half && lead))
+            before = *reinterpret_cast<const uintx4_any_t *>(src + d - half);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            other[i] = (d + i < half ? after : before)[i / 2] >> 16 * (i % 2) & 0xFFFFu;
+        if (d < half && d + 8 > half && !lead) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (d + i >= half) other[i] = src[d + i - half];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int e = min(d + i, R - 1);
+        const bool first = interleaved ? i % 2 == 0 : e < half;
+        const int pair = interleaved ? e / 2 : first ? e : e - half;
+        const float a = bf16_to_f32(x[i]) * cosine[pair], b = bf16_to_f32(other[i]) * sine[pair];
+        out[i] = d + i < R ? f32_to_bf16(first ? a - b : b + a) : x[i];
+    }
+    const uintx4_t w = {out[0] | out[1] << 16, out[2] | out[3] << 16, out[4] | out[5] << 16,
+                        out[6] | out[7] << 16};
+    *reinterpret_cast<uintx4_t *>(dst + d) = w;
 }
 
 template <int MODE>
@@ -87,13 +132,8 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(
         const int rotated = h < n_rotate ? (MODE == kHalf ? half / 8 : rot_dim / 8) : 0;
         const int pieces = h < n_rotate ? rotated + (D - rot_dim) / 8 : D / 8;
         if (MODE == kAny && h < n_rotate) {
-            for (int i = piece0; i < half; i += 1 << width_shift) {
-                const int ia = interleaved ? 2 * i : i, ib = interleaved ? 2 * i + 1 : i + half;
-                const float xa = bf16_to_f32(src[ia]), xb = bf16_to_f32(src[ib]);
-                dst[ia] = static_cast<uint16_t>(f32_to_bf16(xa * cosine[i] - xb * sine[i]));
-                dst[ib] = static_cast<uint16_t>(f32_to_bf16(xa * sine[i] + xb * cosine[i]));
-            }
-            for (int i = rot_dim + piece0; i < D; i += 1 << width_shift) dst[i] = src[i];
+            for (int p = piece0; p < D / 8; p += 1 << width_shift)
+                rotate_any(src, dst, 8 * p, rot_dim, interleaved, h > 0, cosine, sine);
             continue;
         }
         for (int p = piece0; p < pieces; p += 1 << width_shift) {
