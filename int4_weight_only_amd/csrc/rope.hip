@@ -7,8 +7,8 @@
 // bf16, at position 10^5.
 //
 // Memory-bound: qkv is read once, q and the new cache rows are written once. 8 prompts of up to
-// 2048 tokens, 28 + 4 + 4 heads of 128: 239 MB in 41 to 46 us, a large copy's rate or more. One token:
-// 4 us, the launch and two waits for memory (length and page, then the row).
+// 2048 tokens, 28 + 4 + 4 heads of 128: 239 MB in 41 to 46 us, a large copy's rate or more. One
+// token: 4 us, the launch and two waits for memory (length and page, then the row).
 #include "w4_device.h"
 #include "w4_launch.h"
 
