@@ -407,12 +407,11 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
                              reinterpret_cast<const float *>(sv[w]) + row * kRow + d);
             }
             if (whole) {
-                v *= sum > 0.0f ? 1.0f / sum : 0.0f;
+                v *= inverse_sum(sum);
                 store_out4(a.y, b * a.ldy + static_cast<int64_t>(head0 + row) * D + d, v, a.out_f32,
                            wide);
                 if (a.lse && d == 0)
-                    a.lse[static_cast<int64_t>(b) * a.n_heads + head0 + row] =
-                        sum > 0.0f ? m * kLn2 + logf(sum) : -INFINITY;
+                    a.lse[static_cast<int64_t>(b) * a.n_heads + head0 + row] = log_sum(m, sum);
             } else {
                 *reinterpret_cast<floatx4_t *>(part + 2 * slot_rows + row * D + d) = v;
                 if (d == 0) {
@@ -469,9 +468,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvV
     if (tid >= lanes) return;
     for (int q = 1; q < groups; ++q)
         add(sm[q * lanes + tid], sl[q * lanes + tid], so[q * lanes + tid]);
-    v *= l > 0.0f ? 1.0f / l : 0.0f;
+    v *= inverse_sum(l);
     store_out4(a.y, b * a.ldy + static_cast<int64_t>(head) * D + d, v, a.out_f32, wide_rows(a));
-    if (a.lse && d == 0) a.lse[pair] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+    if (a.lse && d == 0) a.lse[pair] = log_sum(m, l);
 }
 
 Plan plan_of(int n_heads, const KvView &c, int window, int sinks) {

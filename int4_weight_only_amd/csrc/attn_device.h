@@ -53,6 +53,13 @@ __device__ __forceinline__ bool wide_rows(const AttnArgs &a) {
     return (a.ldy & 3) == 0 && (reinterpret_cast<uintptr_t>(a.y) & 15) == 0;
 }
 
+// What sums weighted by l in all are multiplied with, and ln of l weights of maximum m (log2 units).
+// l is 0 where no key is seen; one that is NaN, from a NaN score, stays NaN in both.
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float log_sum(float m, float l) {
+    return l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+}
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Sum over lanes 0 .. own lane (row shifts, then the rows' totals to the rows after them).

@@ -532,8 +532,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
             }
         return;
     }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    if (a.lse && half == 0) a.lse[pair] = l > 0.0f ? M * kLn2 + logf(l) : -INFINITY;
+    const float inv = inverse_sum(l);
+    if (a.lse && half == 0) a.lse[pair] = log_sum(M, l);
     const int64_t base = token * a.ldy + static_cast<int64_t>(head) * D;
     const bool wide = wide_rows(a);
 #pragma unroll
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int 
         const float m1 = p.ml[2 * pair], l1 = p.ml[2 * pair + 1];
         const floatx4_t v1 = *reinterpret_cast<const floatx4_t *>(p.o + pair * D + at);
         // (a split without keys has written no weighted sums)
-        add(m1, l1, l1 > 0.0f ? v1 : floatx4_t(0.0f));
+        add(m1, l1, l1 == 0.0f ? floatx4_t(0.0f) : v1);
     }
 #pragma unroll
     for (int o = LANES; o < kWave; o <<= 1) {
@@ -586,8 +586,8 @@ __global__ void __launch_bounds__(256) attn_prefill_join_kernel(AttnArgs a, int 
         add(__shfl_xor(m, o, kWave), __shfl_xor(l, o, kWave), v1);
     }
     if (lane >= LANES) return;
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-    if (a.lse && lane == 0) a.lse[pair] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+    const float inv = inverse_sum(l);
+    if (a.lse && lane == 0) a.lse[pair] = log_sum(m, l);
     if (col < D)
         store_out4(a.y, token * a.ldy + (pair - token * a.n_heads) * D + col, v * inv, a.out_f32,
                    wide_rows(a));

@@ -1,0 +1,102 @@
+"""Values at the edges of the number formats in the operators between a decoder layer's linears:
+infinities and NaN in keys, values and residuals, scores far from zero.  The plain forms are those of
+tests/layer_reference.py or the definition written out; a row that does not see a value that is not
+finite keeps every bit of its result."""
+import numpy as np
+import pytest
+import torch
+
+import int4_weight_only_amd as w4
+from tests import layer_reference as ref
+from tests.test_gpu_layer import Paged, bf16, close, f64
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+def run(cache, q, q_start, **kw):
+    """(y fp32 [T][H][D], lse); q_start None: one token per sequence."""
+    kw = dict(kw, out_dtype=w4.W4_OUT_F32, want_lse=True)
+    if q_start is None:
+        y, lse = w4.w4_attn_decode(q, *cache.args(), **kw)
+    else:
+        y, lse = w4.w4_attn_prefill(q, *cache.args(), torch.from_numpy(q_start).cuda(), **kw)
+    torch.cuda.synchronize()
+    return y.reshape(q.shape[0], -1, cache.D).cpu(), lse.cpu()
+
+
+def same_classes(got, want, bound, what):
+    """NaN where the definition gives NaN, its infinities, and finite values within the bound."""
+    assert np.array_equal(np.isnan(got), np.isnan(want)), f"{what}: NaN in other places"
+    inf = np.isinf(want)
+    assert np.array_equal(np.isinf(got), inf), f"{what}: infinities in other places"
+    assert np.array_equal(got[inf], want[inf]), f"{what}: infinities of the other sign"
+    ok = np.isfinite(want)
+    close(np.where(ok, got, 0.0), np.where(ok, want, 0.0), np.where(ok, bound, 1.0), what)
+
+
+def poisoned(seed, lens, nq, H, n_kv, D, page, spots, window=0, sinks=0):
+    """Runs a case before and after values that are not finite enter it at `spots`, (sequence,
+    position, key-value head, "k" or "v", dim, value)."""
+    rng = np.random.default_rng(seed)
+    cache = Paged(rng, lens, page, n_kv, D)
+    cache.fill(rng, [range(n) for n in lens])
+    counts = [1] * len(lens) if nq is None else nq
+    starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    T, G = int(starts[-1]), H // n_kv
+    q = bf16(rng.normal(size=(T, H * D))).cuda()
+    kw = dict(window=window, sinks=sinks)
+    q_start = None if nq is None else starts
+    before, lse_before = run(cache, q, q_start, **kw)
+    for b, pos, hk, kind, d, value in spots:
+        (cache.k if kind == "k" else cache.v)[cache.table[b][pos // page], pos % page, hk, d] = value
+    y, lse = run(cache, q, q_start, **kw)
+    k, v, table = cache.host()
+    with np.errstate(invalid="ignore"):
+        wy, wl, a, ds, count = ref.attention(f64(q), k, v, table, lens, starts, H,
+                                             float(np.float32(D ** -0.5)), window, sinks)
+        bound = ref.attention_bound(a, ds, count, 16 if nq is None else 8)
+    same_classes(f64(y), wy, bound, "y")
+    assert np.array_equal(np.isnan(f64(lse)), np.isnan(wl)), "lse: NaN in other places"
+    ok = np.isfinite(wl)
+    assert np.all(np.abs(np.where(ok, f64(lse) - wl, 0))[ok]
+                  <= (2 * ds + 2.0 ** -20 + (count + 4) * ref.F32 * 2 + 2.0 ** -22 * np.abs(wl))[ok])
+    # rows that see none of the spots: not a bit changes
+    seen = np.zeros((T, H), dtype=bool)
+    for t, b, pos in ref.rows_of(starts, lens, cache.cols * page):
+        vis = set(ref.visible(pos, window, sinks).tolist())
+        for sb, spos, hk, *_ in spots:
+            if sb == b and spos in vis:
+                seen[t, hk * G:(hk + 1) * G] = True
+    assert seen.any() and not seen.all()
+    assert torch.equal(y[~seen], before[~seen]) and torch.equal(lse[~seen], lse_before[~seen])
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (128, 4), (64, 16), (80, 16), (256, 32)])
+def test_nan_scores(D, page):
+    """y and lse are NaN for the rows that see the key, in both forms, in shares and splits too."""
+    spots = [(0, 190, 1, "k", 3, NAN), (1, 69, 0, "k", 0, NAN)]
+    poisoned([46, D], [300, 70], [300, 70], 6, 2, D, page, spots)
+    poisoned([47, D], [300, 70, 1], None, 6, 2, D, page, spots)
+    poisoned([48, D], [9000, 70, 33], None, 6, 2, D, page, spots)
+    poisoned([49, D], [5000], [20], 4, 2, D, page, [(0, 4985, 0, "k", 5, NAN)])
+
+
+@pytest.mark.parametrize("form", [None, 3])
+def test_nan_rows_with_any_output_stride(form):
+    rng = np.random.default_rng(65)
+    T = 3 if form is None else 3 * form
+    cache = Paged(rng, [50, 60, 70], 16, 1, 64)
+    cache.fill(rng, [range(50), range(60), range(70)])
+    cache.k[cache.table[1][2], 0, 0, 0] = NAN  # position 32 of sequence 1
+    q = bf16(rng.normal(size=(T, 128))).cuda()
+    starts = torch.arange(0, T + 1, T // 3, dtype=torch.int32).cuda()
+    for pad in (0, 1):
+        out = torch.zeros((T, 128 + pad), dtype=torch.bfloat16, device="cuda")
+        if form is None:
+            w4.w4_attn_decode(q, *cache.args(), out=out)
+        else:
+            w4.w4_attn_prefill(q, *cache.args(), starts, out=out)
+        nan = torch.isnan(out[:, :128]).cpu().reshape(3, -1)
+        assert nan[1].all() and not nan[0].any() and not nan[2].any()
