@@ -35,6 +35,36 @@ __device__ __forceinline__ uintx2_t lds_read_transposed(const uint16_t *p) {
                               __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)(p)));
 }
 
+// Eight bf16 values without the ones that are infinite or NaN (0 in their place), and those by kind:
+// bf16 1 for infinity, MINUS for minus infinity, NAN_ for NaN (bf16 bit patterns), 0 elsewhere.
+template <uint32_t MINUS, uint32_t NAN_>
+__device__ __forceinline__ uintx4_t split_values(uintx4_t v, uintx4_t *kind) {
+    uintx4_t finite;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t fin = 0, k = 0;
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+            const uint32_t e = v[i] >> h & 0xFFFFu;
+            const uint32_t of = e == 0x7F80u ? 0x3F80u : e == 0xFF80u ? MINUS : NAN_;
+            const bool odd = (e & 0x7F80u) == 0x7F80u;
+            fin |= (odd ? 0u : e) << h;
+            k |= (odd ? of : 0u) << h;
+        }
+        finite[i] = fin;
+        (*kind)[i] = k;
+    }
+    return finite;
+}
+// Adds n counted values to a sum: infinities in the places of 1, minus infinities in those of MINUS
+// (a power of two above the count), NaN from NAN_ on.
+template <int MINUS, int NAN_>
+__device__ __forceinline__ float add_kinds(float sum, int n) {
+    sum = n & (MINUS - 1) ? sum + INFINITY : sum;
+    sum = n & (NAN_ - MINUS) ? sum - INFINITY : sum;
+    return n >= NAN_ ? __builtin_nanf("") : sum;
+}
+
 // Four consecutive elements of an output row, from element idx (a multiple of 4) on. `wide`: the
 // output's base and rows allow one store.
 __device__ __forceinline__ void store_out4(void *y, int64_t idx, floatx4_t v, bool out_f32,

@@ -136,6 +136,12 @@ __device__ __forceinline__ void tile_barrier() {
     phase_fence();
 }
 
+// The same value, as if unknown: nothing computed from it is taken for what was computed before.
+__device__ __forceinline__ int unknown(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
+}
+
 // Partial results of split `part`: per (token row, head) D weighted sums, and the pair (maximum in
 // log2 units, sum of weights).
 struct Partials {
@@ -188,9 +194,39 @@ __device__ __forceinline__ void load_to_lds(const void *from, uint16_t *lds) {
 // tokens, 16 heads over 4 of 256, window 1024, pages of 16: by spans 197 us, by rows 218.)
 enum { kAnyPages = 0, kSpanPages = 1, kTilePages = 2 };
 
-template <int DP, int KT, int PAGES>
-__global__ void __launch_bounds__(kWaves * 64)
-__attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvView c, int splits) {
+struct Args {
+    AttnArgs a;
+    KvView c;
+    int splits;
+};
+// The kernel's arguments, read once more: its only parameter is at the start of their segment.
+__device__ __forceinline__ Args args_again() {
+    typedef const __attribute__((address_space(4))) uint32_t *const_ptr;
+    uint64_t p = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(p));
+    static_assert(sizeof(Args) % 4 == 0, "words");
+    uint32_t words[sizeof(Args) / 4];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(Args) / 4); ++i)
+        words[i] = reinterpret_cast<const_ptr>(p)[i];
+    Args args;
+    __builtin_memcpy(&args, words, sizeof(Args));
+    return args;
+}
+
+// One tile of rows over the keys of one split.
+//
+// A weight of 0 hides only a finite value from a row: 0 times infinity is NaN. So a block in which any
+// sum is not finite at the end goes through its keys again with ANY set: one tile at a time, 32
+// dims at a time, and values that are not finite reach only the rows that see them. Rows that see
+// none come out the same, bit for bit. The second pass reads its arguments anew and takes its lane
+// number as if unknown: whatever the two passes shared would occupy registers throughout, and the
+// first pass' loop lost its order of reads or spilled (one prompt of 2048 tokens, 28 heads over 4
+// of 128: 54 us for 49; 2 chunks of up to 4096, 256 dims, window 1024: 201 us for 176).
+template <int DP, int KT, int PAGES, bool ANY>
+__device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c, int splits,
+                                             uint16_t *sk0, uint16_t *sk1, uint16_t *sv0,
+                                             uint16_t *sv1, int *votes) {
     constexpr int BM = kTileRows, NW = kWaves;
     constexpr int kChunks = DP / 8;                    // 16-byte chunks of a row
     constexpr int kSpan = 64 / kChunks;                // rows a wave stages in one instruction
@@ -198,15 +234,9 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
     static_assert(kLoads * NW * kSpan == KT, "every wave stages the same number of rows");
     using L = TileLayout<DP>;
     constexpr int DT = DP / 32, KS = DP / 16, SUB = KT / 32;
-    // (arrays of their own: the compiler then sees that a direct load on its way into one does not
-    // touch the others, and does not wait for it before it reads them)
-    __shared__ __attribute__((aligned(16))) uint16_t sk0[KT / kSpan * L::kKeyBlock];
-    __shared__ __attribute__((aligned(16))) uint16_t sk1[KT / kSpan * L::kKeyBlock];
-    __shared__ __attribute__((aligned(16))) uint16_t sv0[KT / kSpan * L::kValueBlock];
-    __shared__ __attribute__((aligned(16))) uint16_t sv1[KT / kSpan * L::kValueBlock];
-
-    const int lane = threadIdx.x & 63;
-    const int wid = uniform(threadIdx.x >> 6);
+    const int tid = ANY ? unknown(threadIdx.x) : threadIdx.x;
+    const int lane = tid & 63;
+    const int wid = uniform(tid >> 6);
     const int G = a.n_heads / c.n_kv, D = c.head_dim;
     const int hk = blockIdx.x % c.n_kv, part = blockIdx.x / c.n_kv % splits;
     Tile t;
@@ -319,7 +349,8 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
             const uint32_t other = (safe - k0) * c.slot_stride;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                w.off[i] = visible(k0 + span_at(i) + my_row) ? seen_off[i] : other;
+                // (uniform, to be added here: else each sum has a register of its own throughout)
+                w.off[i] = visible(uniform(k0 + span_at(i)) + my_row) ? seen_off[i] : other;
         } else {
             const bool all = all_seen(k0);
 #pragma unroll
@@ -407,6 +438,36 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
                         __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);
                 }
     };
+    // The same for 32 dims from 32 d on, where values may be infinite or NaN. The finite ones go
+    // through the product above; the others, counted by kind for each row that sees them (1 for
+    // infinity, 32 for minus infinity, 1024 for NaN; 16 keys a step), are added as what they are.
+    const auto weigh_any = [&](const uint16_t *v, int d) __attribute__((always_inline)) {
+        const int r = 4 * half + (lane & 15) / 4, c = 2 * (lane >> 4 & 1) + (lane & 3) / 2;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const uint16_t *p = v + (32 * u + 16 * st) / kSpan * L::kValueBlock +
+                                    L::value_at(r, 4 * d + c) + 4 * (lane & 1);
+                const uintx2_t v0 = lds_read_transposed(p);
+                const uintx2_t v1 = lds_read_transposed(p + 8 / kSpan * L::kValueBlock);
+                const uintx4_t all = {v0[0], v0[1], v1[0], v1[1]};
+                uintx4_t kind, seen;  // seen: bf16 ones where weights are
+                const uintx4_t fin = split_values<0x4200u, 0x4480u>(all, &kind);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    seen[i] = (s[u][8 * st + 2 * i] != -INFINITY ? 0x3F80u : 0) |
+                              (s[u][8 * st + 2 * i + 1] != -INFINITY ? 0x3F800000u : 0);
+                o[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8_t, fin), pf[u][st], o[0], 0, 0, 0);
+                const floatx16_t n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                    __builtin_bit_cast(bf16x8_t, kind), __builtin_bit_cast(bf16x8_t, seen),
+                    floatx16_t(0.0f), 0, 0, 0);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[0][i] = add_kinds<32, 1024>(o[0][i], static_cast<int>(n[i]));
+            }
+    };
     // Hides the scores of the keys that a row does not see, and raises M; returns the factor that
     // the sums so far have to take if it rose for any row (`rose`).
     const auto raise = [&](int it, bool *rose) __attribute__((always_inline)) {
@@ -479,6 +540,76 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
         tile_barrier();
     };
 
+    const auto block_any = [&](bool v) {  // (called once)
+        const bool mine = __any(v);
+        if (lane == 0) votes[wid] = mine;
+        __syncthreads();
+        bool any = false;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) any |= votes[w] != 0;
+        return any;
+    };
+    // What is written of a row: its maximum and sum of weights (or its lse), and 32 of its dims.
+    const auto pair_of_row = [&] { return (t.q0 + tok) * static_cast<int64_t>(a.n_heads) + head; };
+    const auto write_row = [&]() __attribute__((always_inline)) {
+        l += other_half(l);
+        if (row >= t.rows || half != 0) return;
+        const int64_t pair = pair_of_row();
+        if (splits > 1) {
+            const Partials p = partials(a.work, a.T * a.n_heads, splits, part, D);
+            p.ml[2 * pair] = M;
+            p.ml[2 * pair + 1] = l;
+        } else if (a.lse) {
+            a.lse[pair] = log_sum(M, l);
+        }
+    };
+    const auto write_dims = [&](int d, const floatx16_t &o) __attribute__((always_inline)) {
+        // (splits without keys: their sum is 0, the weighted sums are not read)
+        if (row >= t.rows || (splits > 1 && n_iter == 0)) return;
+        const Partials p = partials(a.work, a.T * a.n_heads, splits, part, D);
+        const int64_t token = t.q0 + tok;
+        const int64_t base = token * a.ldy + static_cast<int64_t>(head) * D;
+        const float inv = inverse_sum(l);
+        const bool wide = wide_rows(a);
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const int col = 32 * d + 8 * g + 4 * half;
+            if (col >= D) continue;
+            floatx4_t v = {o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]};
+            if (splits > 1)
+                *reinterpret_cast<floatx4_t *>(p.o + pair_of_row() * D + col) = v;
+            else
+                store_out4(a.y, base + col, v * inv, a.out_f32, wide);
+        }
+    };
+
+    if constexpr (ANY) {
+        for (int d = 0; 32 * d < D; ++d) {
+            M = kNoMax;
+            l = 0.0f;
+            o[0] = floatx16_t(0.0f);
+            for (int i = 0; i < n_iter; ++i) {
+                look_up(i);
+                locate(i, newest);
+                fetch(head_k, newest, k_col, sk0, L::kKeyBlock);
+                fetch(head_v, newest, v_col, sv0, L::kValueBlock);
+                tile_barrier();
+                scores(sk0);
+                bool rose;
+                const float f = raise(i, &rose);
+                if (rose) o[0] *= f;
+                weights();
+                weigh_any(sv0, d);
+                tile_barrier();
+            }
+            if (d == 0)
+                write_row();
+            else
+                l += other_half(l);
+            write_dims(d, o[0]);
+        }
+        return;
+    }
     if (n_iter > 0) {
         look_up(0);
         locate(0, newest);
@@ -509,44 +640,37 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(AttnArgs a, KvVie
             ++it;
         }
         weigh(it & 1 ? sv1 : sv0);
-    }
 
-    l += other_half(l);
-    if (row >= t.rows) return;
-    const int64_t token = t.q0 + tok, pair = token * a.n_heads + head;
-    if (splits > 1) {
-        const Partials p = partials(a.work, a.T * a.n_heads, splits, part, D);
-        if (half == 0) {
-            p.ml[2 * pair] = M;
-            p.ml[2 * pair + 1] = l;
-        }
-        if (n_iter == 0) return;  // (its sum is 0: the weighted sums are not read)
+        float odd = 0.0f;
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const int col = 32 * d + 8 * g + 4 * half;
-                if (col < D)
-                    *reinterpret_cast<floatx4_t *>(p.o + pair * D + col) = floatx4_t{
-                        o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
-            }
-        return;
-    }
-    const float inv = inverse_sum(l);
-    if (a.lse && half == 0) a.lse[pair] = log_sum(M, l);
-    const int64_t base = token * a.ldy + static_cast<int64_t>(head) * D;
-    const bool wide = wide_rows(a);
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int col = 32 * d + 8 * g + 4 * half;
-            if (col >= D) continue;
-            floatx4_t v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = o[d][4 * g + i] * inv;
-            store_out4(a.y, base + col, v, a.out_f32, wide);
+            for (int i = 0; i < 16; ++i) odd = fmaf(o[d][i], 0.0f, odd);
+        if (__builtin_expect(block_any(odd != 0.0f), 0)) {
+            const Args again = args_again();
+            prefill_tile<DP, KT, PAGES, true>(again.a, again.c, again.splits, sk0, sk0, sv0, sv0,
+                                              votes);
+            return;
         }
+    }
+
+    write_row();
+#pragma unroll
+    for (int d = 0; d < DT; ++d) write_dims(d, o[d]);
+}
+
+template <int DP, int KT, int PAGES>
+__global__ void __launch_bounds__(kWaves * 64)
+__attribute__((amdgpu_waves_per_eu(2, 2))) attn_prefill_kernel(Args args) {
+    using L = TileLayout<DP>;
+    // (arrays of their own: the compiler then sees that a direct load on its way into one does not
+    // touch the others, and does not wait for it before it reads them)
+    __shared__ __attribute__((aligned(16))) uint16_t sk0[KT / L::kSpan * L::kKeyBlock];
+    __shared__ __attribute__((aligned(16))) uint16_t sk1[KT / L::kSpan * L::kKeyBlock];
+    __shared__ __attribute__((aligned(16))) uint16_t sv0[KT / L::kSpan * L::kValueBlock];
+    __shared__ __attribute__((aligned(16))) uint16_t sv1[KT / L::kSpan * L::kValueBlock];
+    __shared__ int votes[kWaves];
+    prefill_tile<DP, KT, PAGES, false>(args.a, args.c, args.splits, sk0, sk1, sv0, sv1, votes);
 }
 
 // Joins the splits of a (token row, head), one wave each: groups of LANES lanes, 4 dims a lane,
@@ -618,15 +742,13 @@ Plan plan_of(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
 template <int DP, int KT>
 void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t stream) {
     const dim3 grid(static_cast<unsigned>(p.tiles * c.n_kv * p.splits)), block(kWaves * 64);
+    const Args args = {a, c, p.splits};
     if (c.page_mask >= KT - 1)
-        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kTilePages>), grid, block, 0, stream, a, c,
-                           p.splits);
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kTilePages>), grid, block, 0, stream, args);
     else if (c.page_mask >= 7)
-        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kSpanPages>), grid, block, 0, stream, a, c,
-                           p.splits);
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kSpanPages>), grid, block, 0, stream, args);
     else
-        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kAnyPages>), grid, block, 0, stream, a, c,
-                           p.splits);
+        hipLaunchKernelGGL((attn_prefill_kernel<DP, KT, kAnyPages>), grid, block, 0, stream, args);
 }
 
 }  // namespace

@@ -83,6 +83,32 @@ def test_nan_scores(D, page):
     poisoned([49, D], [5000], [20], 4, 2, D, page, [(0, 4985, 0, "k", 5, NAN)])
 
 
+PROMPT_SPOTS = [(0, 150, 0, "v", 5, INF), (0, 160, 0, "v", 7, NAN), (0, 171, 1, "v", 0, -INF),
+                (0, 180, 1, "v", 0, INF), (0, 190, 1, "k", 3, NAN), (1, 69, 0, "v", 2, -INF)]
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (128, 16), (128, 1), (64, 64), (64, 8), (80, 16),
+                                    (256, 32), (256, 8), (192, 1), (24, 4)])
+def test_prompt_rows_before_a_value_that_is_not_finite(D, page):
+    poisoned([50, D, page], [300, 70], [300, 70], 6, 2, D, page, PROMPT_SPOTS)
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (80, 16), (256, 32)])
+def test_prompt_rows_past_a_value_that_is_not_finite(D, page):
+    """The window leaves it behind; sinks stay in sight."""
+    poisoned([51, D], [300, 70], [300, 70], 6, 2, D, page, PROMPT_SPOTS, window=21, sinks=3)
+    poisoned([52, D], [300, 70], [300, 70], 6, 2, D, page, [(0, 2, 1, "v", 1, INF)], window=21,
+             sinks=3)
+
+
+@pytest.mark.parametrize("D,page", [(128, 64), (128, 16), (64, 64), (256, 32)])
+def test_few_rows_over_a_long_cache_with_values_that_are_not_finite(D, page):
+    """The keys split over workgroups."""
+    spots = [(0, 4990, 0, "v", 5, INF), (0, 4995, 1, "v", 7, NAN), (0, 4993, 1, "v", 1, -INF)]
+    poisoned([53, D], [5000], [20], 4, 2, D, page, spots)
+    poisoned([55, D], [5000], [20], 4, 2, D, page, [(0, 1990, 0, "v", 5, -INF)], window=3000)
+
+
 @pytest.mark.parametrize("form", [None, 3])
 def test_nan_rows_with_any_output_stride(form):
     rng = np.random.default_rng(65)
