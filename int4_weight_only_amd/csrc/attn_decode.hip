@@ -35,6 +35,8 @@ constexpr int kTile = 32;   // keys of a tile
 constexpr int kWaves = 4;
 constexpr int kRows = 16;   // query heads of a workgroup
 constexpr int kSlack = 8;   // log2 of how far a weight may pass 1 before the sums are rescaled
+// Values that are not finite, counted over a tile's keys: bf16 64 for minus infinity, 4096 for NaN.
+constexpr uint32_t kMinus = 0x4280u, kNan = 0x4580u;
 
 // The visible keys of a sequence, as tiles.
 struct Keys {
@@ -282,9 +284,9 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
         float M = kNoMax, l = 0.0f;
 
         // One tile; with MORE, the wave's next tile is fetched on the way, and the one after that
-        // looked up.
-        const auto step = [&](auto more, int t) {
-            constexpr bool MORE = decltype(more)::value;
+        // looked up; with ANY, values may be infinite or NaN.
+        const auto step = [&](auto more, auto any, int t) {
+            constexpr bool MORE = decltype(more)::value, ANY = decltype(any)::value;
             const int k0 = keys.start(t), after = min(t + 2 * kWaves, t1 - 1);
             if constexpr (MORE) look_up(after);
             floatx4_t s[2];
@@ -300,9 +302,11 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
             if constexpr (MORE) fetch_k();
             phase_fence();
 #pragma unroll
-            for (int i = 0; i < kVLoads; ++i)
-                *reinterpret_cast<uintx4_t *>(
-                    &my_v[(i * kVRows + v_row) * kRow + 8 * (lane % kChunks)]) = rv[i];
+            for (int i = 0; i < kVLoads; ++i) {
+                uintx4_t kind, *to = reinterpret_cast<uintx4_t *>(
+                                   &my_v[(i * kVRows + v_row) * kRow + 8 * (lane % kChunks)]);
+                *to = ANY ? split_values<kMinus, kNan>(rv[i], &kind) : rv[i];
+            }
             phase_fence();
             __builtin_amdgcn_wave_barrier();
             if constexpr (MORE) {
@@ -359,6 +363,40 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
             }
             asm volatile("" ::: "memory");
             __builtin_amdgcn_wave_barrier();
+            if constexpr (ANY) {
+                // the values that are not finite, counted by kind for the keys that are seen
+                uintx4_t seen;  // bf16 ones where weights are
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 4; i += 2)
+                        seen[2 * u + i / 2] =
+                            (ok[u][i] && s[u][i] != -INFINITY ? 0x3F80u : 0) |
+                            (ok[u][i + 1] && s[u][i + 1] != -INFINITY ? 0x3F800000u : 0);
+#pragma unroll
+                for (int i = 0; i < kVLoads; ++i) {
+                    uintx4_t kind;
+                    split_values<kMinus, kNan>(rv[i], &kind);
+                    *reinterpret_cast<uintx4_t *>(
+                        &my_v[(i * kVRows + v_row) * kRow + 8 * (lane % kChunks)]) = kind;
+                }
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const uintx2_t v0 = lds_read_transposed(vp + 16 * d);
+                    const uintx2_t v1 = lds_read_transposed(vp + 16 * kRow + 16 * d);
+                    const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
+                    const floatx4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        __builtin_bit_cast(bf16x8_t, vv), __builtin_bit_cast(bf16x8_t, seen),
+                        floatx4_t(0.0f), 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[d][i] = add_kinds<64, 4096>(o[d][i], static_cast<int>(n[i]));
+                }
+                asm volatile("" ::: "memory");
+                __builtin_amdgcn_wave_barrier();
+            }
         };
         int t = t0 + wid;
         if (t < t1) {
@@ -370,11 +408,32 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
             locate(min(t + kWaves, t1 - 1));
             if (t + kWaves < t1) {
                 do {
-                    step(std::true_type{}, t);
+                    step(std::true_type{}, std::false_type{}, t);
                     t += kWaves;
                 } while (t + kWaves < t1);
             }
-            step(std::false_type{}, t);
+            step(std::false_type{}, std::false_type{}, t);
+        }
+        // An infinite value times the lower part of its weight, or a weight of 0 (where the row
+        // that stands in for a hidden one holds it), is not that infinity. So a wave whose sums are
+        // not finite goes through its tiles again, its values split into finite ones and others.
+        float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd[i] = fmaf(o[d][i], 0.0f, odd[i]);
+        if (__builtin_expect(__any(odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f), 0)) {
+            M = kNoMax;
+            l = 0.0f;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[d] = floatx4_t(0.0f);
+            for (t = t0 + wid; t < t1; t += kWaves) {
+                look_up(t);
+                locate(t);
+                fetch_k();
+                fetch_v();
+                step(std::false_type{}, std::true_type{}, t);
+            }
         }
 
         // Join the waves: lane (g, r) holds dims 16 d + 4 g + 0..3 of head r.

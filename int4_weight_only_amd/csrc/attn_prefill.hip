@@ -641,12 +641,12 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
         }
         weigh(it & 1 ? sv1 : sv0);
 
-        float odd = 0.0f;
+        float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int d = 0; d < DT; ++d)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) odd = fmaf(o[d][i], 0.0f, odd);
-        if (__builtin_expect(block_any(odd != 0.0f), 0)) {
+            for (int i = 0; i < 16; ++i) odd[i % 4] = fmaf(o[d][i], 0.0f, odd[i % 4]);
+        if (__builtin_expect(block_any(odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f), 0)) {
             const Args again = args_again();
             prefill_tile<DP, KT, PAGES, true>(again.a, again.c, again.splits, sk0, sk0, sv0, sv0,
                                               votes);

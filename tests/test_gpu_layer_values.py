@@ -109,6 +109,19 @@ def test_few_rows_over_a_long_cache_with_values_that_are_not_finite(D, page):
     poisoned([55, D], [5000], [20], 4, 2, D, page, [(0, 1990, 0, "v", 5, -INF)], window=3000)
 
 
+@pytest.mark.parametrize("D,page", [(128, 64), (128, 4), (64, 16), (80, 16), (256, 32), (192, 1)])
+@pytest.mark.parametrize("lens", [(300, 70, 1), (9000, 70, 33)])
+def test_decode_with_values_that_are_not_finite(D, page, lens):
+    """In a share of its own and in one that is joined; the keys that fill up a tile repeat a key."""
+    n = lens[0]
+    spots = [(0, n - 1, 0, "v", 5, INF), (0, n // 2, 0, "v", 7, -INF), (0, n - 2, 1, "v", 0, NAN),
+             (0, 0, 1, "v", 1, INF), (0, 3, 1, "v", 1, -INF), (1, 69, 0, "v", 2, -INF)]
+    poisoned([56, D, n], list(lens), None, 6, 2, D, page, spots)
+    poisoned([57, D, n], list(lens), None, 6, 2, D, page, [(0, n - 3, 1, "k", 5, NAN),
+                                                           (0, 9, 0, "v", 2, -INF)])
+    poisoned([58, D, n], list(lens), None, 34, 2, D, page, spots[:2], window=n - 1)
+
+
 @pytest.mark.parametrize("form", [None, 3])
 def test_nan_rows_with_any_output_stride(form):
     rng = np.random.default_rng(65)
