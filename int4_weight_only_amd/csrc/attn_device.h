@@ -16,7 +16,9 @@ typedef uint32_t uintx4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kNoMax = -1e30f;  // running maximum before the first key (finite: no inf - inf)
+// Running maximum before the first key: the lowest finite number, so that no score lies below it and
+// no infinity is subtracted from another.
+constexpr float kNoMax = -3.40282347e38f;
 
 // Two fp32 values as bf16 (round to nearest even) in one dword, the first in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {

@@ -122,6 +122,42 @@ def test_decode_with_values_that_are_not_finite(D, page, lens):
     poisoned([58, D, n], list(lens), None, 34, 2, D, page, spots[:2], window=n - 1)
 
 
+TOPS = [-1e9, -1e31, -2.0 ** 126]
+
+def one_dim_scores(form, D, products, scale, seed):
+    """Queries and keys along one dim, so that a score is one product of two bf16 values, exact in
+    fp32: key j of the sequence has the score scale * products[j][0] * products[j][1]."""
+    rng = np.random.default_rng(seed)
+    n = len(products)
+    cache = Paged(rng, [n], 16, 1, D)
+    cache.fill(rng, [range(n)])
+    for j, (_, kv) in enumerate(products):
+        cache.k[cache.table[0][j // 16], j % 16, 0] = bf16(np.eye(D)[1] * kv).cuda()
+    q = bf16(np.tile(np.eye(D)[1] * products[0][0], (1 if form is None else form, 2))).cuda()
+    starts = None if form is None else np.array([0, form], dtype=np.int32)
+    y, lse = run(cache, q, starts, scale=scale)
+    T = q.shape[0]
+    k, v, table = cache.host()
+    wy, wl, a, _, count = ref.attention(f64(q), k, v, table, [n], np.array([0, T]), 2,
+                                        float(np.float32(scale)), 0, 0)
+    # scores are exact or their differences so large that no rounding matters
+    bound = ref.attention_bound(a, np.zeros(wl.shape), count, 16 if form is None else 8)
+    close(f64(y), wy, bound, "y")
+    assert np.all(np.abs(f64(lse) - wl) <= 2.0 ** -20 + (count + 4) * ref.F32 * 2
+                  + 2.0 ** -22 * np.abs(wl))
+
+
+@pytest.mark.parametrize("form,top", [(None, top) for top in TOPS])
+def test_scores_far_from_zero(form, top):
+    """Keys of the largest score share the weight, however far from zero the scores are."""
+    rng = np.random.default_rng([60, abs(int(top)) % 1000003])
+    top = float(bf16(np.array([top])).item())
+    low = 2.0 * top if top < 0 else 0.5 * top
+    for D in (64, 128, 256):
+        products = [(1.0, top if j < 40 or rng.random() < 0.5 else low) for j in range(150)]
+        one_dim_scores(form, D, products, 1.0, [61, D])
+
+
 @pytest.mark.parametrize("form", [None, 3])
 def test_nan_rows_with_any_output_stride(form):
     rng = np.random.default_rng(65)
