@@ -37,6 +37,7 @@ namespace {
 
 constexpr int kWaves = 4, kTileRows = 32 * kWaves;
 constexpr int kSlack = 8;
+constexpr float kFar = 1 << 20;
 
 // A block's rows: of sequence `seq`, stacked rows row0 .. row0 + BM - 1 of `rows`; token row q0 and
 // position pos0 of stacked row 0.
@@ -219,7 +220,8 @@ __device__ __forceinline__ Args args_again() {
 // A weight of 0 hides only a finite value from a row: 0 times infinity is NaN. So a block in which any
 // sum is not finite at the end goes through its keys again with ANY set: one tile at a time, 32
 // dims at a time, and values that are not finite reach only the rows that see them. Rows that see
-// none come out the same, bit for bit. The second pass reads its arguments anew and takes its lane
+// none come out the same, bit for bit. So does a block with a row whose scores are so large that
+// their rounding matters (see `weights`). The second pass reads its arguments anew and takes its lane
 // number as if unknown: whatever the two passes shared would occupy registers throughout, and the
 // first pass' loop lost its order of reads or spilled (one prompt of 2048 tokens, 28 heads over 4
 // of 128: 54 us for 49; 2 chunks of up to 4096, 256 dims, window 1024: 201 us for 176).
@@ -321,10 +323,18 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
         int64_t base[kBases];
         uint32_t off[kLoads];
     };
-    uint32_t seen_off[kLoads];  // the offsets in a tile whose rows are all seen
+    // The offsets in a tile whose rows are all seen. At 256 dims, where registers are short, the part
+    // that is uniform is added at the use. (2 chunks of up to 4096 tokens, window 1024: 170 us so,
+    // 188 with a register each; at 128 dims one prompt of 2048: 51.5 so, 49.9 with registers.)
+    constexpr bool kAddUniform = DP > 128 && PAGES == kTilePages;
+    uint32_t row_off[kAddUniform ? 1 : kLoads];
 #pragma unroll
-    for (int i = 0; i < kLoads; ++i)
-        seen_off[i] = ((PAGES == kTilePages ? span_at(i) : 0) + my_row) * c.slot_stride;
+    for (int i = 0; i < (kAddUniform ? 1 : kLoads); ++i)
+        row_off[i] = ((PAGES == kTilePages && !kAddUniform ? span_at(i) : 0) + my_row) *
+                     c.slot_stride;
+    const auto seen_off = [&](int i) {
+        return kAddUniform ? row_off[0] + uniform(span_at(i) * c.slot_stride) : row_off[i];
+    };
     int entry[kBases];
     const auto look_up = [&](int it) {  // the page table entries of a tile
         const int k0 = tile_key(it);
@@ -350,7 +360,7 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
                 // (uniform, to be added here: else each sum has a register of its own throughout)
-                w.off[i] = visible(uniform(k0 + span_at(i)) + my_row) ? seen_off[i] : other;
+                w.off[i] = visible(uniform(k0 + span_at(i)) + my_row) ? seen_off(i) : other;
         } else {
             const bool all = all_seen(k0);
 #pragma unroll
@@ -363,7 +373,7 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
                     const int first_row = safe >= s0 && safe < s0 + kSpan ? s0 : safe;
                     w.base[i] = page_offset(entry[i]) +
                                 static_cast<int64_t>((first_row & c.page_mask) * c.slot_stride);
-                    w.off[i] = vis ? seen_off[i] : (safe - first_row) * c.slot_stride;
+                    w.off[i] = vis ? seen_off(i) : (safe - first_row) * c.slot_stride;
                 } else {
                     const int from = vis ? p : safe;
                     w.base[i] = page_offset(read_const(table + (from >> c.page_shift)));
@@ -505,14 +515,29 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
         }
         return f;
     };
+    // A weight's exponent comes from one multiply-add, while M is rounded: by as much as the exponent
+    // may be off (2^-4 at kFar; 2^16 at 2^40, which overflows). With ANY, the scores of rows whose
+    // M is beyond kFar are scaled, and so rounded, as M was.
+    const auto is_far = [&] { return fabsf(M) > kFar && M != kNoMax; };
     const auto weights = [&]() __attribute__((always_inline)) {
+        const float k = ANY && is_far() ? 1.0f : cs;
+        if (ANY) {
+#pragma unroll
+            for (int u = 0; u < SUB; ++u)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float scaled = s[u][i] * cs;
+                    asm volatile("" : "+v"(scaled));  // (rounded, not fused with what follows)
+                    s[u][i] = is_far() ? scaled : s[u][i];
+                }
+        }
 #pragma unroll
         for (int u = 0; u < SUB; ++u) {
             uintx4_t x[2];
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], cs, -M));
-                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], cs, -M));
+                const float p0 = __builtin_amdgcn_exp2f(fmaf(s[u][i], k, -M));
+                const float p1 = __builtin_amdgcn_exp2f(fmaf(s[u][i + 1], k, -M));
                 l += p0 + p1;
                 x[i / 8][i % 8 / 2] = pack_bf16(p0, p1);
             }
@@ -646,9 +671,10 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) odd[i % 4] = fmaf(o[d][i], 0.0f, odd[i % 4]);
-        if (__builtin_expect(block_any(odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f), 0)) {
-            const Args again = args_again();
-            prefill_tile<DP, KT, PAGES, true>(again.a, again.c, again.splits, sk0, sk0, sv0, sv0,
+        const bool again = odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f || is_far();
+        if (__builtin_expect(block_any(again), 0)) {
+            const Args args = args_again();
+            prefill_tile<DP, KT, PAGES, true>(args.a, args.c, args.splits, sk0, sk0, sv0, sv0,
                                               votes);
             return;
         }

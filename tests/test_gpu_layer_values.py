@@ -122,7 +122,7 @@ def test_decode_with_values_that_are_not_finite(D, page, lens):
     poisoned([58, D, n], list(lens), None, 34, 2, D, page, spots[:2], window=n - 1)
 
 
-TOPS = [-1e9, -1e31, -2.0 ** 126]
+TOPS = [1e9, 1e12, 1e20, 2.0 ** 110, -1e9, -1e12, -1e29, -1e31, -2.0 ** 126]
 
 def one_dim_scores(form, D, products, scale, seed):
     """Queries and keys along one dim, so that a score is one product of two bf16 values, exact in
@@ -147,7 +147,7 @@ def one_dim_scores(form, D, products, scale, seed):
                   + 2.0 ** -22 * np.abs(wl))
 
 
-@pytest.mark.parametrize("form,top", [(None, top) for top in TOPS])
+@pytest.mark.parametrize("form,top", [(form, top) for form in (None, 1, 40) for top in TOPS])
 def test_scores_far_from_zero(form, top):
     """Keys of the largest score share the weight, however far from zero the scores are."""
     rng = np.random.default_rng([60, abs(int(top)) % 1000003])
