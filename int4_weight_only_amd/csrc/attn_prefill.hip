@@ -286,8 +286,9 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
     floatx16_t o[DT];
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = floatx16_t(0.0f);
-    // (a scale of 0 as one that moves no weight, so that hidden scores of -inf stay -inf)
-    const float cs = fmaxf(a.scale * kLog2e, 1e-37f);
+    // (a scale of 0 as the smallest number, which moves no weight, so that hidden scores of -inf stay
+    // -inf)
+    const float cs = fmaxf(a.scale * kLog2e, 0x1p-149f);
     const int before = a.window > 0 ? pos - a.window : -1;  // newest position out of the window
     float M = kNoMax, l = 0.0f;
 

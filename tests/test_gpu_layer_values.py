@@ -158,6 +158,15 @@ def test_scores_far_from_zero(form, top):
         one_dim_scores(form, D, products, 1.0, [61, D])
 
 
+@pytest.mark.parametrize("form", [None, 1, 40])
+def test_scales_near_the_smallest_number(form):
+    big = 2.0 ** 63
+    rng = np.random.default_rng(62)
+    for scale in (2.0 ** -126, 2.0 ** -127, 0.0):
+        products = [(big, big * rng.integers(-4, 5) / 4) for _ in range(150)]
+        one_dim_scores(form, 64, products, scale, 63)
+
+
 @pytest.mark.parametrize("form", [None, 3])
 def test_nan_rows_with_any_output_stride(form):
     rng = np.random.default_rng(65)
