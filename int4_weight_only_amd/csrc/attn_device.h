@@ -2,6 +2,7 @@
 // reads, output stores, sums and maxima over lanes.
 #pragma once
 
+#include "bf16_device.h"
 #include "w4_device.h"
 #include "w4_launch.h"
 
@@ -19,15 +20,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Running maximum before the first key: the lowest finite number, so that no score lies below it and
 // no infinity is subtracted from another.
 constexpr float kNoMax = -3.40282347e38f;
-
-// Two fp32 values as bf16 (round to nearest even) in one dword, the first in the low half.
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    bf16x2_t r;
-    r[0] = static_cast<__bf16>(a);
-    r[1] = static_cast<__bf16>(b);
-    return __builtin_bit_cast(uint32_t, r);
-}
 
 // Four bf16 rows of 16 columns, transposed on the way out of LDS: in each group of 16 lanes, lane i
 // addresses the 8 bytes at columns 4 (i % 4) of row i / 4 and receives column i of the four rows.
@@ -71,14 +63,22 @@ __device__ __forceinline__ float add_kinds(float sum, int n) {
 // output's base and rows allow one store.
 __device__ __forceinline__ void store_out4(void *y, int64_t idx, floatx4_t v, bool out_f32,
                                            bool wide) {
-    if (!wide) {
+    float *y32 = static_cast<float *>(y) + idx;
+    uint16_t *y16 = static_cast<uint16_t *>(y) + idx;
+    const uintx2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+    if (wide) {
+        if (out_f32)
+            *reinterpret_cast<floatx4_t *>(y32) = v;
+        else
+            *reinterpret_cast<uintx2_t *>(y16) = w;
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store_out(y, idx + i, v[i], out_f32);
-    } else if (out_f32) {
-        *reinterpret_cast<floatx4_t *>(static_cast<float *>(y) + idx) = v;
-    } else {
-        const uintx2_t w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-        *reinterpret_cast<uintx2_t *>(static_cast<uint16_t *>(y) + idx) = w;
+    for (int i = 0; i < 4; ++i) {
+        if (out_f32)
+            y32[i] = v[i];
+        else
+            y16[i] = static_cast<uint16_t>(w[i / 2] >> 16 * (i % 2));
     }
 }
 __device__ __forceinline__ bool wide_rows(const AttnArgs &a) {

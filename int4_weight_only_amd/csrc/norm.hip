@@ -5,6 +5,7 @@
 // once; the two sums of squares are fp32 sums over the row's threads. A row of up to 512 elements
 // belongs to one wave (no barrier), a longer one to a workgroup. 8192 rows of 3584 with an fp32
 // residual stream move 352 MB in 68 us: 5.2 TB/s, a large copy's rate.
+#include "bf16_device.h"
 #include "w4_device.h"
 #include "w4_launch.h"
 
@@ -54,7 +55,7 @@ __device__ __forceinline__ void load8(const float *p, int n, float *v) { read8(p
 __device__ __forceinline__ void store8(uint16_t *p, int n, const float *v) {
     uint16_t e[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = static_cast<uint16_t>(f32_to_bf16(v[i]));
+    for (int i = 0; i < 8; ++i) e[i] = to_bf16(v[i]);
     write8(p, n, e);
 }
 __device__ __forceinline__ void store8(float *p, int n, const float *v) { write8(p, n, v); }

@@ -9,6 +9,7 @@
 // Memory-bound: qkv is read once, q and the new cache rows are written once. 8 prompts of up to
 // 2048 tokens, 28 + 4 + 4 heads of 128: 239 MB in 41 to 46 us, a large copy's rate or more. One
 // token: 4 us, the launch and two waits for memory (length and page, then the row).
+#include "bf16_device.h"
 #include "w4_device.h"
 #include "w4_launch.h"
 
@@ -48,7 +49,7 @@ __device__ __forceinline__ void unpack8(const uint16_t *p, float *v) {
 __device__ __forceinline__ void pack8(uint16_t *p, const float *v) {
     uintx4_t w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f32_to_bf16(v[2 * i]) | f32_to_bf16(v[2 * i + 1]) << 16;
+    for (int i = 0; i < 4; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<uintx4_t *>(p) = w;
 }
 
@@ -88,7 +89,7 @@ __device__ __forceinline__ void rotate_any(const uint16_t *src, uint16_t *dst, i
         const bool first = interleaved ? i % 2 == 0 : e < half;
         const int pair = interleaved ? e / 2 : first ? e : e - half;
         const float a = bf16_to_f32(x[i]) * cosine[pair], b = bf16_to_f32(other[i]) * sine[pair];
-        out[i] = d + i < R ? f32_to_bf16(first ? a - b : b + a) : x[i];
+        out[i] = d + i < R ? to_bf16(first ? a - b : b + a) : x[i];
     }
     const uintx4_t w = {out[0] | out[1] << 16, out[2] | out[3] << 16, out[4] | out[5] << 16,
                         out[6] | out[7] << 16};

@@ -122,6 +122,9 @@ def test_decode_with_values_that_are_not_finite(D, page, lens):
     poisoned([58, D, n], list(lens), None, 34, 2, D, page, spots[:2], window=n - 1)
 
 
+# ------------------------------------------------------------------------------- scores
+
+
 TOPS = [1e9, 1e12, 1e20, 2.0 ** 110, -1e9, -1e12, -1e29, -1e31, -2.0 ** 126]
 
 def one_dim_scores(form, D, products, scale, seed):
@@ -165,6 +168,42 @@ def test_scales_near_the_smallest_number(form):
     for scale in (2.0 ** -126, 2.0 ** -127, 0.0):
         products = [(big, big * rng.integers(-4, 5) / 4) for _ in range(150)]
         one_dim_scores(form, 64, products, scale, 63)
+
+
+# ------------------------------------------------------------------------------- rounding to bf16
+
+
+def test_nan_residuals_stay_nan():
+    """Whatever bits a NaN of the fp32 residual holds, its row of y is NaN, and no other."""
+    d = 40
+    r = torch.zeros((4, d), dtype=torch.float32) + 1.5
+    r.view(torch.int32)[0, 3] = -1  # all bits
+    r.view(torch.int32)[1, 9] = 0x7FFFFFFF
+    r.view(torch.int32)[2, 0] = 0x7F800001
+    w = torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    x = torch.zeros((4, d), dtype=torch.bfloat16, device="cuda")
+    for args in ((x, r.cuda(), w), (None, r.cuda(), w)):
+        y, ro = w4.w4_residual_norm(*args)
+        assert torch.isnan(y[:3]).all() and torch.isfinite(y[3]).all()
+        assert torch.equal(torch.isnan(ro.cpu()), torch.isnan(r))
+
+
+def test_residuals_round_to_nearest_even():
+    """r' = r + x in bf16, bit for bit: every finite bf16 value plus zero, and sums of values whose
+    exponents lie up to 20 apart (ties among them)."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    every = bits.view(torch.bfloat16)
+    every = every[torch.isfinite(every)].cuda()
+    every = every[:every.numel() // 64 * 64].reshape(-1, 64)
+    w = torch.ones(64, dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(w4.w4_residual_norm(torch.zeros_like(every), every, w)[1].float(),
+                       every.float())
+    rng = np.random.default_rng(64)
+    r = bf16(rng.integers(-255, 256, size=(4096, 64)) * 2.0 ** rng.integers(-10, 10, (4096, 64)))
+    x = bf16(rng.integers(-255, 256, size=(4096, 64)) * 2.0 ** rng.integers(-10, 10, (4096, 64)))
+    want = (r.float() + x.float()).bfloat16()
+    got = w4.w4_residual_norm(x.cuda(), r.cuda(), w)[1]
+    assert torch.equal(got.cpu().float(), want.float())
 
 
 @pytest.mark.parametrize("form", [None, 3])
