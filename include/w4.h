@@ -408,7 +408,9 @@ int w4_rope_frequencies(int rot_dim, int scaling, double base, double factor, do
  *             each of head_dim; ldqkv % 8 == 0, 16-byte aligned (the output of a w4 linear)
  *   q_start   int32 [n_seqs + 1], or NULL: one token per sequence (T = n_seqs)
  *   inv_freq  fp32 [rot_dim / 2], rot_dim even, 2 .. head_dim;  factor  finite
- *   q         bf16 [T][ldq], ldq >= n_heads * head_dim, ldq % 8 == 0, 16-byte aligned
+ *   q         bf16 [T][ldq], ldq >= n_heads * head_dim, ldq % 8 == 0, 16-byte aligned.  It must not
+ *             overlap the rows of qkv (W4_ERR_SHAPE; columns of one buffer beside them are fine),
+ *             nor may the cache: one thread's output is another one's input.
  * Tokens at negative positions, or whose page table entry lies outside the cache, are not
  * appended; their q row is written all the same.
  */
@@ -427,6 +429,7 @@ int w4_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int n_heads,
  *   scale  finite, >= 0
  *   y      [n_seqs][ldy], ldy >= n_heads * head_dim, element type out_dtype, naturally aligned
  *   lse    fp32 [n_seqs][n_heads] or NULL
+ *   y, lse and work must overlap neither what the call reads nor each other (not checked)
  *   work   device memory of at least w4_attn_decode_work_bytes bytes, 16-byte aligned, as for
  *          w4_gemv_ws; may be NULL when that size is 0
  * Long caches are split over several compute units and joined in order (deterministic).
@@ -468,7 +471,7 @@ size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cac
  *   gate      bf16 [T][ldg], or one vector [d] for all tokens with ldg = 0, or NULL
  *   alpha, weight_offset  finite;  eps  finite, >= 0
  *   r_out     as r, [T][ldr_out]; may be r itself (with ldr_out = ldr), else no overlap
- *   y         bf16 [T][ldy]
+ *   y         bf16 [T][ldy]; no overlap with the other arrays (not checked)
  * d <= W4_NORM_MAX_D (W4_ERR_RANGE beyond).  Leading dimensions are >= d and otherwise free;
  * pointers are naturally aligned.  (Rows that start at 16-byte boundaries are read faster.)
  */

@@ -571,7 +571,7 @@ def w4_rope_append(qkv, n_heads, k_cache, v_cache, page_table, kv_len, inv_freq,
     """Rotary positions on the fused projection qkv bf16 [T][(n_heads + 2 n_kv) head_dim]; the
     rotated keys and the values are written to the cache, the rotated queries returned
     ([T][n_heads * head_dim]).  kv_len counts the T tokens already; q_start int32 [n_seqs + 1] gives
-    each sequence's rows (None: one token per sequence)."""
+    each sequence's rows (None: one token per sequence).  out must not overlap qkv."""
     _need(qkv, "qkv", torch.bfloat16, dim=2)
     dev = qkv.device
     _need(inv_freq, "inv_freq", torch.float32, dev, 1)

@@ -24,6 +24,21 @@ int guarded(F &&launch) {
     }
 }
 
+// Do T rows of `wa` elements from a on, `lda` apart, share an element with T rows of `wb` from b on,
+// `ldb` apart (ld >= w)? Columns of one buffer (lda == ldb) may interleave; rows of different
+// lengths may not.
+bool rows_overlap(const uint16_t *a, int64_t lda, int64_t wa, const uint16_t *b, int64_t ldb,
+                  int64_t wb, int64_t T) {
+    const int64_t gap =  // elements from a's first to b's
+        (reinterpret_cast<intptr_t>(b) - reinterpret_cast<intptr_t>(a)) / 2;
+    if (gap >= (T - 1) * lda + wa || -gap >= (T - 1) * ldb + wb) return false;
+    if (T == 1 || lda != ldb) return true;
+    // row i of b begins in column `col` of row i + rows of a
+    const int64_t rows = gap >= 0 ? gap / lda : -((lda - 1 - gap) / lda), col = gap - rows * lda;
+    return (col < wa && rows > -T && rows < T) ||
+           (col + wb > lda && rows + 1 > -T && rows + 1 < T);
+}
+
 int check_cache(const w4_kv_cache *c, int n_heads, w4::KvView *view) {
     if (!c || !c->k || !c->v || !c->page_table || !c->kv_len) return W4_ERR_NULL;
     if (c->n_pages < 1 || c->n_kv_heads < 1 || c->head_dim < 1 || c->page_size < 1 ||
@@ -176,6 +191,9 @@ int w4_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int n_heads,
     if (!aligned(qkv, 16) || ldqkv % 8 != 0 || !aligned(q, 16) || ldq % 8 != 0 ||
         !aligned(inv_freq, 4) || (q_start && !aligned(q_start, 4)))
         return W4_ERR_ALIGN;
+    if (rows_overlap(qkv, ldqkv, (n_heads + 2 * static_cast<int64_t>(view.n_kv)) * D, q, ldq,
+                     n_heads * D, T))
+        return W4_ERR_SHAPE;
     return guarded([&] {
         return w4::launch_rope_append(qkv, T, ldqkv, n_heads, q_start, inv_freq, rot_dim,
                                       layout == W4_ROPE_INTERLEAVED, factor, view, q, ldq,
