@@ -434,8 +434,9 @@ int w4_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int n_heads,
  *          w4_gemv_ws; may be NULL when that size is 0
  * Long caches are split over several compute units and joined in order (deterministic).
  * w4_attn_decode_work_bytes reads only sizes, no array; 0 for arguments the call rejects.
- * Limits (W4_ERR_RANGE beyond them): n_seqs * n_heads < 2^31, and n_seqs * n_heads times the
- * number of 32-key tiles that table_cols pages can hold < 2^31.
+ * Limits (W4_ERR_RANGE beyond them): n_seqs * n_heads times one more than the number of 32-key tiles
+ * that table_cols pages can hold < 2^31 - 2^16; and the 2^24 - 1 workgroups of a launch, enough for
+ * n_seqs * n_heads up to 2^24 - 2^16 at any length.
  */
 int w4_attn_decode(const uint16_t *q, int64_t ldq, int n_heads, const w4_kv_cache *cache,
                    float scale, int64_t window, int64_t sinks, void *y, int64_t ldy,
@@ -448,7 +449,8 @@ size_t w4_attn_decode_work_bytes(int n_heads, const w4_kv_cache *cache, int64_t 
  * each at its own position: prompts, chunks of prompts, or several new tokens per sequence.
  *   q      bf16 [T][ldq];  q_start int32 [n_seqs + 1];  y [T][ldy];  lse fp32 [T][n_heads] or NULL
  *   the other arguments as for w4_attn_decode.
- * Limits: T * n_heads and n_seqs * n_heads below 2^31 (W4_ERR_RANGE).  The softmax weights enter
+ * Limits (W4_ERR_RANGE): T * n_heads and n_seqs * n_heads below 2^31, and T * n_heads / 128 +
+ * n_seqs * n_kv_heads below 2^24, the workgroups of a launch.  The softmax weights enter
  * the second product as bf16, their sum in fp32.
  */
 int w4_attn_prefill(const uint16_t *q, int64_t T, int64_t ldq, int n_heads,

@@ -206,7 +206,7 @@ size_t w4_attn_decode_work_bytes(int n_heads, const w4_kv_cache *cache, int64_t 
     w4::KvView view;
     w4::AttnArgs a{};
     if (check_cache(cache, n_heads, &view) || check_mask(window, sinks, view, &a) ||
-        !w4::attn_decode_supported(n_heads, view))
+        !w4::attn_decode_supported(n_heads, view, a.window, a.sinks))
         return 0;
     return w4::attn_decode_work_bytes(n_heads, view, a.window, a.sinks);
 }
@@ -219,7 +219,7 @@ int w4_attn_decode(const uint16_t *q, int64_t ldq, int n_heads, const w4_kv_cach
     if (int st = check_attn(q, cache ? cache->n_seqs : 1, ldq, n_heads, nullptr, cache, scale,
                             window, sinks, y, ldy, out_dtype, lse, work, &view, &a))
         return st;
-    if (!w4::attn_decode_supported(n_heads, view)) return W4_ERR_RANGE;
+    if (!w4::attn_decode_supported(n_heads, view, a.window, a.sinks)) return W4_ERR_RANGE;
     if (int st = check_work(w4::attn_decode_work_bytes(n_heads, view, a.window, a.sinks), work,
                             work_bytes))
         return st;
@@ -232,7 +232,8 @@ size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cac
     w4::KvView view;
     w4::AttnArgs a{};
     if (T < 1 || T > W4_MAX_DIM || check_cache(cache, n_heads, &view) ||
-        check_mask(window, sinks, view, &a))
+        check_mask(window, sinks, view, &a) ||
+        !w4::attn_prefill_supported(T, n_heads, view, a.window, a.sinks))
         return 0;
     return w4::attn_prefill_work_bytes(T, n_heads, view, a.window, a.sinks);
 }
@@ -247,6 +248,7 @@ int w4_attn_prefill(const uint16_t *q, int64_t T, int64_t ldq, int n_heads,
     if (int st = check_attn(q, T, ldq, n_heads, q_start, cache, scale, window, sinks, y, ldy,
                             out_dtype, lse, work, &view, &a))
         return st;
+    if (!w4::attn_prefill_supported(T, n_heads, view, a.window, a.sinks)) return W4_ERR_RANGE;
     if (int st = check_work(w4::attn_prefill_work_bytes(T, n_heads, view, a.window, a.sinks),
                             work, work_bytes))
         return st;

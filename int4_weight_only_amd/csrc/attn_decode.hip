@@ -574,9 +574,13 @@ void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t strea
 
 }  // namespace
 
-bool attn_decode_supported(int n_heads, const KvView &c) {
-    const int64_t units = static_cast<int64_t>(c.n_seqs) * n_heads;  // at least
-    return units <= INT32_MAX / (c.capacity / kTile + 1);
+bool attn_decode_supported(int n_heads, const KvView &c, int window, int sinks) {
+    // the tiles of all units, and their division into shares (most_tiles): in 31 bits
+    const int64_t pairs = static_cast<int64_t>(c.n_seqs) * n_heads;  // units at most
+    if (pairs > (INT32_MAX - (1 << 16)) / (c.capacity / kTile + 1)) return false;
+    const Plan p = plan_of(n_heads, c, window, sinks);
+    return p.grid <= static_cast<int64_t>(kMaxThreads) / (kWaves * 64) &&
+           (p.whole_units || pairs <= static_cast<int64_t>(kMaxThreads) / kJoinThreads);
 }
 
 size_t attn_decode_work_bytes(int n_heads, const KvView &c, int window, int sinks) {

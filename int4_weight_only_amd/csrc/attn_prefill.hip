@@ -780,6 +780,12 @@ void launch(const Plan &p, const AttnArgs &a, const KvView &c, hipStream_t strea
 
 }  // namespace
 
+bool attn_prefill_supported(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
+    // (so T G, which the kernel rounds up to tiles, stays below 2^31 too)
+    const Plan p = plan_of(T, n_heads, c, window, sinks);
+    return p.tiles * c.n_kv * p.splits <= static_cast<int64_t>(kMaxThreads) / (kWaves * 64);
+}
+
 size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &c, int window, int sinks) {
     const Plan p = plan_of(T, n_heads, c, window, sinks);
     if (p.splits == 1) return 0;

@@ -148,9 +148,22 @@ __global__ void __launch_bounds__(NT == kWave ? 4 * kWave : NT) residual_norm_ke
 template <typename R, int NT, int NV>
 void launch_nt(const NormArgs &a, hipStream_t stream) {
     constexpr int kRowsPerBlock = NT == kWave ? 4 : 1;
-    const dim3 grid(static_cast<unsigned>((a.T + kRowsPerBlock - 1) / kRowsPerBlock));
-    hipLaunchKernelGGL((residual_norm_kernel<R, NT, NV>), grid, dim3(kRowsPerBlock * NT), 0, stream,
-                       a);
+    // A launch has fewer than 2^32 threads: more rows (2^23 of 4096, say) take several.
+    constexpr int64_t kMostRows = static_cast<int64_t>(kMaxThreads / (kRowsPerBlock * NT)) *
+                                  kRowsPerBlock;
+    const auto from = [](auto *p, int64_t elements) { return p ? p + elements : p; };
+    for (int64_t t = 0; t < a.T; t += kMostRows) {
+        NormArgs part = a;
+        part.T = a.T - t < kMostRows ? a.T - t : kMostRows;
+        part.x = from(a.x, t * a.ldx);
+        part.r = from(static_cast<const R *>(a.r), t * a.ldr);
+        part.gate = from(a.gate, t * a.ldg);
+        part.r_out = from(static_cast<R *>(a.r_out), t * a.ldr_out);
+        part.y = from(a.y, t * a.ldy);
+        const dim3 grid(static_cast<unsigned>((part.T + kRowsPerBlock - 1) / kRowsPerBlock));
+        hipLaunchKernelGGL((residual_norm_kernel<R, NT, NV>), grid, dim3(kRowsPerBlock * NT), 0,
+                           stream, part);
+    }
 }
 
 // One chunk of 8 elements a thread, as far as 512 threads go: what a thread holds it also waits

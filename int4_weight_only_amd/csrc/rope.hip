@@ -190,6 +190,7 @@ hipError_t launch_rope_append(const uint16_t *qkv, int64_t T, int64_t ldqkv, int
     while ((1 << shift) < pieces) ++shift;
     int threads = (n_heads + 2 * c.n_kv) << shift;
     threads = threads >= kThreads ? kThreads : (threads + kWave - 1) / kWave * kWave;
+    if (T > static_cast<int64_t>(kMaxThreads) / threads) threads = kThreads / 2;  // (T = 2^24)
     const int il = interleaved ? 1 : 0;
     if (mode == kHalf)
         return launch<kHalf>(T, threads, stream, qkv, ldqkv, n_heads, q_start, inv_freq, rot_dim,

@@ -10,6 +10,9 @@
 
 namespace w4 {
 
+// Threads of one launch, at most.
+constexpr uint32_t kMaxThreads = UINT32_MAX;
+
 hipError_t launch_pack(const float *w, int64_t d_out, int64_t d_in, int64_t ldw, int64_t span,
                        int64_t n_groups, int64_t k_pad, int mode, uint8_t *qweight,
                        uint16_t *scales, uint16_t *zeros, hipStream_t stream);
@@ -153,7 +156,9 @@ struct AttnArgs {
     float *lse;
     void *work;
 };
-bool attn_decode_supported(int n_heads, const KvView &cache);  // the sizes it counts in 31 bits
+// Sizes that the kernels count in 31 bits and that one launch takes.
+bool attn_decode_supported(int n_heads, const KvView &cache, int window, int sinks);
+bool attn_prefill_supported(int64_t T, int n_heads, const KvView &cache, int window, int sinks);
 size_t attn_decode_work_bytes(int n_heads, const KvView &cache, int window, int sinks);
 hipError_t launch_attn_decode(const AttnArgs &a, const KvView &cache, hipStream_t stream);
 size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &cache, int window, int sinks);
