@@ -517,7 +517,7 @@ def w4a8_linear(x, qweight, s_w, bias, d_in, out_dtype=W4_OUT_BF16, want_acc=Fal
 def w4_rope_frequencies(rot_dim, scaling=W4_ROPE_PLAIN, base=10000.0, factor=1.0, context=1.0):
     """(inv_freq fp32 [rot_dim / 2], amplitude) of rotary positions for a context scaling (host
     only; move inv_freq to the GPU once)."""
-    inv_freq = torch.empty(max(rot_dim, 2) // 2, dtype=torch.float32)
+    inv_freq = torch.empty(max(rot_dim, 2) // 2, dtype=torch.float32, device="cpu")
     amplitude = ctypes.c_float()
     _check("w4_rope_frequencies", _lib.w4_rope_frequencies(
         rot_dim, scaling, base, factor, context, _ptr(inv_freq), ctypes.byref(amplitude)))

@@ -2,6 +2,9 @@
 enqueued (fake device addresses, as in test_layer_abi.py)."""
 import numpy as np
 
+import torch
+
+import int4_weight_only_amd as w4
 from tests.test_layer_abi import RANGE, SHAPE, E, cache, decode, lib, prefill, rope
 
 
@@ -54,3 +57,10 @@ def test_decode_counts_tiles_in_31_bits():
     c = one_head(255, page_size=32, cols=8421503)
     assert decode(c, H=1, ldq=8, ldy=8) == RANGE
     assert lib.w4_attn_decode_work_bytes(1, c, 0, 0) == 0
+
+
+def test_rope_frequencies_are_host_memory_under_any_default_device():
+    want, _ = w4.w4_rope_frequencies(64)
+    with torch.device("meta"):
+        got, _ = w4.w4_rope_frequencies(64)
+    assert got.device.type == "cpu" and torch.equal(got, want)
