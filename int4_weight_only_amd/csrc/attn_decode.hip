@@ -116,10 +116,16 @@ __device__ __forceinline__ Shares find_shares(const AttnArgs &a, const KvView &c
     return s;
 }
 
-// A share's partial result: `rows` maxima (log2 units), `rows` sums of weights, then rows x D
-// weighted sums.
-__device__ __forceinline__ float *partial(void *work, int64_t group, int rows, int D) {
-    return static_cast<float *>(work) + group * rows * (D + 2);
+// A share's partial result: rows x D weighted sums (16-byte rows: D is a multiple of 8), and after
+// those of all shares its `rows` maxima (log2 units) and `rows` sums of weights.
+struct Partial {
+    float *o, *m, *l;
+};
+__device__ __forceinline__ Partial partial(void *work, const Plan &p, int64_t group, int rows,
+                                           int D) {
+    float *base = static_cast<float *>(work);
+    float *m = base + static_cast<int64_t>(p.grid) * rows * D + group * 2 * rows;
+    return {base + group * rows * D, m, m + rows};
 }
 
 // The rows of a sequence without keys: zeros.
@@ -450,7 +456,7 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
         __syncthreads();
         const bool wide = wide_rows(a);
         const int slot_rows = min(G, kRows);
-        float *part = partial(a.work, blockIdx.x, slot_rows, D);
+        const Partial part = partial(a.work, plan, blockIdx.x, slot_rows, D);
         for (int e = tid; e < n_rows * (DP / 4); e += kWaves * 64) {
             const int row = e / (DP / 4), d = e % (DP / 4) * 4;
             if (d >= D) continue;
@@ -472,10 +478,10 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
                 if (a.lse && d == 0)
                     a.lse[static_cast<int64_t>(b) * a.n_heads + head0 + row] = log_sum(m, sum);
             } else {
-                *reinterpret_cast<floatx4_t *>(part + 2 * slot_rows + row * D + d) = v;
+                *reinterpret_cast<floatx4_t *>(part.o + row * D + d) = v;
                 if (d == 0) {
-                    part[row] = m;
-                    part[slot_rows + row] = sum;
+                    part.m[row] = m;
+                    part.l[row] = sum;
                 }
             }
         }
@@ -497,7 +503,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvV
     const int unit = head / G * row_tiles + in_group / kRows, row = in_group % kRows;
     const int n = s.shares;
     const auto part = [&](int i) {
-        return partial(a.work, s.first + unit * n + i, rows, D);
+        return partial(a.work, plan, s.first + unit * n + i, rows, D);
     };
     const int tid = threadIdx.x;
     const int lanes = D / 4;                  // threads over the dims, 4 each
@@ -515,9 +521,8 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, KvV
     if (grp < groups) {
 #pragma unroll 4
         for (int i = grp; i < n; i += groups) {
-            const float *p = part(i);
-            add(p[row], p[rows + row],
-                *reinterpret_cast<const floatx4_t *>(p + 2 * rows + row * D + d));
+            const Partial p = part(i);
+            add(p.m[row], p.l[row], *reinterpret_cast<const floatx4_t *>(p.o + row * D + d));
         }
         so[tid] = v;
         sm[tid] = m;
