@@ -3,16 +3,14 @@
 // include/w4.h; nothing here allocates device memory or synchronizes.
 #include <hip/hip_runtime.h>
 
-#include <mutex>
-#include <string>
-#include <vector>
+#include <atomic>
 
 #include "../../include/w4.h"
 #include "w4_launch.h"
 
 namespace {
 
-thread_local std::string g_last_hip_error;
+thread_local const char *g_last_hip_error = "";  // (static storage)
 
 using w4::hip_fail;
 
@@ -78,7 +76,7 @@ const char *w4_status_string(int status) {
     }
 }
 
-const char *w4_last_hip_error(void) { return g_last_hip_error.c_str(); }
+const char *w4_last_hip_error(void) { return g_last_hip_error; }
 
 int w4_packed_layout(int64_t d_out, int64_t d_in, int group_size, int64_t *k_pad,
                      int64_t *n_groups, size_t *qweight_bytes) {
@@ -364,26 +362,23 @@ int w4a8_linear(const uint16_t *x, int64_t M, int64_t ldx, const uint8_t *qweigh
 
 namespace w4 {
 
-int hip_fail(hipError_t err) {
+int hip_fail(hipError_t err) noexcept {
     g_last_hip_error = hipGetErrorString(err);
     return W4_ERR_HIP;
 }
 
-int device_cu_count() {
-    static std::mutex mu;
-    static std::vector<int> cache;
-    int dev = 0;
+int device_cu_count() noexcept {
+    constexpr int kCached = 64;
+    static std::atomic<int> cache[kCached];  // 0: not asked yet
+    int dev = 0, n = 0;
     if (hipGetDevice(&dev) != hipSuccess) return 256;
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev >= static_cast<int>(cache.size())) cache.resize(dev + 1, 0);
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
-            n <= 0)
-            n = 256;
-        cache[dev] = n;
-    }
-    return cache[dev];
+    const bool cached = dev >= 0 && dev < kCached;
+    if (cached && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess ||
+        n <= 0)
+        n = 256;
+    if (cached) cache[dev].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 }  // namespace w4

@@ -13,6 +13,10 @@ namespace {
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Nothing that the entry points call outside of `guarded` may throw.
+static_assert(noexcept(w4::device_cu_count()) && noexcept(w4::hip_fail(hipSuccess)),
+              "no exception passes the C boundary");
+
 // Runs a launcher; neither a HIP error nor a C++ exception passes the C boundary.
 template <typename F>
 int guarded(F &&launch) {

@@ -180,9 +180,10 @@ struct NormArgs {
 hipError_t launch_residual_norm(const NormArgs &a, hipStream_t stream);
 
 // Records the text of a failed HIP call for w4_last_hip_error; returns W4_ERR_HIP.
-int hip_fail(hipError_t err);
+int hip_fail(hipError_t err) noexcept;
 
-// Number of compute units of the current device (cached per device).
-int device_cu_count();
+// Number of compute units of the current device (cached per device). The entry points ask for it
+// outside of any try block.
+int device_cu_count() noexcept;
 
 }  // namespace w4
