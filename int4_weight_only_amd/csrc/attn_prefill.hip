@@ -218,13 +218,15 @@ __device__ __forceinline__ Args args_again() {
 // One tile of rows over the keys of one split.
 //
 // A weight of 0 hides only a finite value from a row: 0 times infinity is NaN. So a block in which any
-// sum is not finite at the end goes through its keys again with ANY set: one tile at a time, 32
+// sum is not finite at the end goes through its keys again with ANY set: one tile at a time, 64
 // dims at a time, and values that are not finite reach only the rows that see them. Rows that see
 // none come out the same, bit for bit. So does a block with a row whose scores are so large that
-// their rounding matters (see `weights`). The second pass reads its arguments anew and takes its lane
-// number as if unknown: whatever the two passes shared would occupy registers throughout, and the
-// first pass' loop lost its order of reads or spilled (one prompt of 2048 tokens, 28 heads over 4
-// of 128: 54 us for 49; 2 chunks of up to 4096, 256 dims, window 1024: 201 us for 176).
+// their rounding matters (see `weights`). (3 prompts of up to 4096 tokens, 28 heads over 4 of 128:
+// 0.30 ms, with one infinity in the longest 0.91, all values NaN 2.5. The check itself costs a call
+// of 77 tokens 0.3 us.) The second pass reads its arguments anew and takes its lane number as if
+// unknown: whatever the two passes shared would occupy registers throughout, and the first pass'
+// loop lost its order of reads or spilled (one prompt of 2048 tokens: 54 us for 49; 2 chunks of up
+// to 4096, 256 dims, window 1024: 201 us for 176).
 template <int DP, int KT, int PAGES, bool ANY>
 __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c, int splits,
                                              uint16_t *sk0, uint16_t *sk1, uint16_t *sv0,
@@ -449,34 +451,43 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
                         __builtin_bit_cast(bf16x8_t, vv), pf[u][st], o[d], 0, 0, 0);
                 }
     };
-    // The same for 32 dims from 32 d on, where values may be infinite or NaN. The finite ones go
-    // through the product above; the others, counted by kind for each row that sees them (1 for
-    // infinity, 32 for minus infinity, 1024 for NaN; 16 keys a step), are added as what they are.
-    const auto weigh_any = [&](const uint16_t *v, int d) __attribute__((always_inline)) {
+    // The same for kAnyDims times 32 dims from 32 d0 on, where values may be infinite or NaN. The
+    // finite ones go through the product above; the others, counted by kind for each row that sees
+    // them (1 for infinity, 32 for minus infinity, 1024 for NaN; 16 keys a step), are added as what
+    // they are.
+    constexpr int kAnyDims = 2;
+    const auto weigh_any = [&](const uint16_t *v, int d0) __attribute__((always_inline)) {
         const int r = 4 * half + (lane & 15) / 4, c = 2 * (lane >> 4 & 1) + (lane & 3) / 2;
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
-                const uint16_t *p = v + (32 * u + 16 * st) / kSpan * L::kValueBlock +
-                                    L::value_at(r, 4 * d + c) + 4 * (lane & 1);
-                const uintx2_t v0 = lds_read_transposed(p);
-                const uintx2_t v1 = lds_read_transposed(p + 8 / kSpan * L::kValueBlock);
-                const uintx4_t all = {v0[0], v0[1], v1[0], v1[1]};
-                uintx4_t kind, seen;  // seen: bf16 ones where weights are
-                const uintx4_t fin = split_values<0x4200u, 0x4480u>(all, &kind);
+                uintx4_t seen;  // bf16 ones where weights are
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     seen[i] = (s[u][8 * st + 2 * i] != -INFINITY ? 0x3F80u : 0) |
                               (s[u][8 * st + 2 * i + 1] != -INFINITY ? 0x3F800000u : 0);
-                o[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8_t, fin), pf[u][st], o[0], 0, 0, 0);
-                const floatx16_t n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                    __builtin_bit_cast(bf16x8_t, kind), __builtin_bit_cast(bf16x8_t, seen),
-                    floatx16_t(0.0f), 0, 0, 0);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[0][i] = add_kinds<32, 1024>(o[0][i], static_cast<int>(n[i]));
+                for (int d = 0; d < kAnyDims; ++d) {
+                    const uint16_t *p = v + (32 * u + 16 * st) / kSpan * L::kValueBlock +
+                                        L::value_at(r, 4 * (d0 + d) + c) + 4 * (lane & 1);
+                    const uintx2_t v0 = lds_read_transposed(p);
+                    const uintx2_t v1 = lds_read_transposed(p + 8 / kSpan * L::kValueBlock);
+                    const uintx4_t all = {v0[0], v0[1], v1[0], v1[1]};
+                    uintx4_t kind;
+                    const uintx4_t fin = split_values<0x4200u, 0x4480u>(all, &kind);
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                        __builtin_bit_cast(bf16x8_t, fin), pf[u][st], o[d], 0, 0, 0);
+                    if (__any((kind[0] | kind[1] | kind[2] | kind[3]) != 0)) {
+                        const floatx16_t n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                            __builtin_bit_cast(bf16x8_t, kind), __builtin_bit_cast(bf16x8_t, seen),
+                            floatx16_t(0.0f), 0, 0, 0);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            o[d][i] = add_kinds<32, 1024>(o[d][i], static_cast<int>(n[i]));
+                    }
+                    phase_fence();
+                }
             }
     };
     // Hides the scores of the keys that a row does not see, and raises M; returns the factor that
@@ -610,10 +621,11 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
     };
 
     if constexpr (ANY) {
-        for (int d = 0; 32 * d < D; ++d) {
+        for (int d0 = 0; 32 * d0 < D; d0 += kAnyDims) {
             M = kNoMax;
             l = 0.0f;
-            o[0] = floatx16_t(0.0f);
+#pragma unroll
+            for (int d = 0; d < kAnyDims; ++d) o[d] = floatx16_t(0.0f);
             for (int i = 0; i < n_iter; ++i) {
                 look_up(i);
                 locate(i, newest);
@@ -623,16 +635,20 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
                 scores(sk0);
                 bool rose;
                 const float f = raise(i, &rose);
-                if (rose) o[0] *= f;
+                if (rose) {
+#pragma unroll
+                    for (int d = 0; d < kAnyDims; ++d) o[d] *= f;
+                }
                 weights();
-                weigh_any(sv0, d);
+                weigh_any(sv0, d0);
                 tile_barrier();
             }
-            if (d == 0)
+            if (d0 == 0)
                 write_row();
             else
                 l += other_half(l);
-            write_dims(d, o[0]);
+#pragma unroll
+            for (int d = 0; d < kAnyDims; ++d) write_dims(d0 + d, o[d]);
         }
         return;
     }
