@@ -349,7 +349,8 @@ int w4a8_gemm(const int8_t *q, const float *s_x, int64_t M, int64_t ldq, const u
  * token that another one sees reach the rows of those that do not see it, infinite or NaN as its key
  * and value may be.  A score that is NaN makes y and lse of its row NaN; a visible value that is NaN
  * or infinite makes its dimension of y what such a sum is (that infinity; NaN for both, and where
- * the weight is too small for fp32).
+ * the weight is too small for fp32).  An infinite element of a visible key may make its score NaN,
+ * and so may scores of 2^127 and more in magnitude.
  *
  * Token rows: sequence b has the rows q_start[b] <= t < q_start[b + 1] (q_start int32
  * [n_seqs + 1], nondecreasing, q_start[0] = 0, q_start[n_seqs] = T), which are its LAST tokens: row

@@ -1,8 +1,10 @@
 // attn_decode.hip -- attention of one new token per sequence over the paged cache.
 //
-// One pass over the keys and values of a sequence (w4_attn_decode), bound by reading them: 4 flop
-// per byte and query head. The G = n_heads / n_kv query heads of a key-value head are the columns
-// of one 16-wide matrix-core tile, so that a key is read once for all of them (16 at a time).
+// One pass over the keys and values of a sequence (w4_attn_decode), bound by reading them: 1 flop
+// per byte and query head (1.5 with the weights in two parts, below). The G = n_heads / n_kv query
+// heads of a key-value head are the columns of one 16-wide matrix-core tile, so that a key is read
+// once for up to 16 of them (more heads read it once per 16: 32 heads over 1, 32 x 4096 keys, 26
+// us).
 //
 //   S^T[key][head] = K Q^T   on v_mfma_f32_16x16x32_bf16; a lane's 16 bytes of a key row are the
 //                            operand as they come from memory
@@ -19,10 +21,10 @@
 // flight), and the waves join in LDS. The shares of a unit that was cut meet in the caller's
 // workspace, and a second kernel joins them in order.
 //
-// 28 heads over 4 of 128: 4 sequences of up to 131072 keys 188 us (5.5 TB/s of keys and values,
-// more than a large copy's 4.9), 32 of up to 8192 64 us (4.3 TB/s). One sequence of 4097 keys takes
-// 11 us: nothing but waits for memory, one after the other (page, keys, partial results), and two
-// launches.
+// 28 heads over 4 of 128: 4 sequences of up to 131072 keys 185 us (5.5 TB/s of keys and values; a
+// large copy reaches 5.0 to 5.5, an elementwise pass 6.3), 32 of up to 8192 63 us (4.4 TB/s). One
+// sequence of 4097 keys takes 11.3 us: nothing but waits for memory, one after the other (page,
+// keys, partial results), and two launches (7.2 and 4.2 us).
 #include <type_traits>
 
 #include "attn_device.h"

@@ -22,11 +22,12 @@
 // A workgroup is four waves, 128 stacked rows; tiles of 64 keys (32 at 256 dims) go from memory
 // straight to LDS, double buffered, one barrier a tile. Two workgroups run on a compute unit, so
 // that one can multiply while the other turns scores into weights. Bound by the sum of both: three
-// prompts of up to 4096 tokens, 28 heads over 4 of 128, take 296 us, 968 TFLOP/s of the 1350 that a
-// large matrix product reaches here, with the matrix cores busy 46 % and the vector units 48 % of
-// the time (32 exponentials, multiply-adds and sums, 16 roundings and 16 maxima a lane for every 32
-// products). Exponentials between the products' instructions of the same wave left the time as it
-// was (320 us for 321 in one run), as did two groups of waves in turns.
+// prompts of up to 4096 tokens, 28 heads over 4 of 128, take 296 to 313 us over runs, 915 to 968
+// TFLOP/s of the 1350 that a large matrix product reaches here, with the matrix cores busy 44 to 46
+// % and the vector units 46 to 48 % of the time (32 exponentials, multiply-adds and sums, 16
+// roundings and 16 maxima a lane for every 32 products). Exponentials between the products'
+// instructions of the same wave left the time as it was (320 us for 321 in one run), as did two
+// groups of waves in turns.
 #include <algorithm>
 
 #include "attn_device.h"
@@ -191,7 +192,7 @@ __device__ __forceinline__ void load_to_lds(const void *from, uint16_t *lds) {
 
 // What lies in one page: a tile (pages of KT slots and more), the rows a wave stages in one
 // instruction (8 at most, aligned: pages of 8 slots and more), or a row. (4 prompts of up to 2048
-// tokens, 28 heads over 4 of 128: pages of 64 121 us, of 32 by spans 135. 2 chunks of up to 4096
+// tokens, 28 heads over 4 of 128: pages of 64 121 us, of 32 by spans 133. 2 chunks of up to 4096
 // tokens, 16 heads over 4 of 256, window 1024, pages of 16: by spans 197 us, by rows 218.)
 enum { kAnyPages = 0, kSpanPages = 1, kTilePages = 2 };
 
@@ -217,8 +218,8 @@ __device__ __forceinline__ Args args_again() {
 
 // One tile of rows over the keys of one split.
 //
-// A weight of 0 hides only a finite value from a row: 0 times infinity is NaN. So a block in which any
-// sum is not finite at the end goes through its keys again with ANY set: one tile at a time, 64
+// A weight of 0 hides only a finite value from a row: 0 times infinity is NaN. So a block in which
+// any sum is not finite at the end goes through its keys again with ANY set: one tile at a time, 64
 // dims at a time, and values that are not finite reach only the rows that see them. Rows that see
 // none come out the same, bit for bit. So does a block with a row whose scores are so large that
 // their rounding matters (see `weights`). (3 prompts of up to 4096 tokens, 28 heads over 4 of 128:
@@ -288,8 +289,8 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
     floatx16_t o[DT];
 #pragma unroll
     for (int i = 0; i < DT; ++i) o[i] = floatx16_t(0.0f);
-    // (a scale of 0 as the smallest number, which moves no weight, so that hidden scores of -inf stay
-    // -inf)
+    // (a scale of 0 as the smallest number, which moves no weight, so that hidden scores of -inf
+    // stay -inf)
     const float cs = fmaxf(a.scale * kLog2e, 0x1p-149f);
     const int before = a.window > 0 ? pos - a.window : -1;  // newest position out of the window
     float M = kNoMax, l = 0.0f;
@@ -326,9 +327,9 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
         int64_t base[kBases];
         uint32_t off[kLoads];
     };
-    // The offsets in a tile whose rows are all seen. At 256 dims, where registers are short, the part
-    // that is uniform is added at the use. (2 chunks of up to 4096 tokens, window 1024: 170 us so,
-    // 188 with a register each; at 128 dims one prompt of 2048: 51.5 so, 49.9 with registers.)
+    // The offsets in a tile whose rows are all seen. At 256 dims, where registers are short, the
+    // part that is uniform is added at the use. (2 chunks of up to 4096 tokens, window 1024: 170 us
+    // so, 188 with a register each; at 128 dims one prompt of 2048: 51.5 so, 49.9 with registers.)
     constexpr bool kAddUniform = DP > 128 && PAGES == kTilePages;
     uint32_t row_off[kAddUniform ? 1 : kLoads];
 #pragma unroll
@@ -527,9 +528,9 @@ __device__ __forceinline__ void prefill_tile(const AttnArgs &a, const KvView &c,
         }
         return f;
     };
-    // A weight's exponent comes from one multiply-add, while M is rounded: by as much as the exponent
-    // may be off (2^-4 at kFar; 2^16 at 2^40, which overflows). With ANY, the scores of rows whose
-    // M is beyond kFar are scaled, and so rounded, as M was.
+    // A weight's exponent comes from one multiply-add, while M is rounded: by as much as the
+    // exponent may be off (2^-4 at kFar; 2^16 at 2^40, which overflows). With ANY, the scores of
+    // rows whose M is beyond kFar are scaled, and so rounded, as M was.
     const auto is_far = [&] { return fabsf(M) > kFar && M != kNoMax; };
     const auto weights = [&]() __attribute__((always_inline)) {
         const float k = ANY && is_far() ? 1.0f : cs;
