@@ -462,6 +462,93 @@ size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cac
                                   int64_t window, int64_t sinks);
 
 /*
+ * w4_attn_shared -- the same attention for sequences that share prefixes (a system prompt, a document,
+ * the question of several samples): the keys of a prefix are read and multiplied once for all rows of
+ * the sequences that share it, not once for each.  The visible keys and the result are those of
+ * w4_attn_decode (q_start NULL: T = n_seqs, one row each) and w4_attn_prefill; only the place of a key
+ * differs: position j of sequence b with prefix g = prefix_of[b] is
+ *   j < prefix length of g:  position j of the prefix, by row g of the prefixes' table
+ *   else:                    position j of the sequence, by its own row of the page table
+ * so that entries of a sequence's row below its prefix are not read, and a prefix may end inside a
+ * page.  kv_len counts the prefix.  A row that stands inside the prefix sees it up to itself.
+ *
+ * w4_prefixes -- the prefixes of a batch; a struct on the host, arrays on the device.
+ *   prefix_of   int32 [n_seqs]: the prefix of each sequence, in any order; a value outside
+ *               [0, n_prefixes) for none
+ *   table       int32 [n_prefixes][ld_table], table_cols entries used: pages of the same cache.  (Rows
+ *               of the page table itself serve as well.)  Entries outside the cache as there.
+ *   len         int32 [n_prefixes]: keys of each prefix; below 0 as 0, above table_cols * page_size
+ *               as that
+ *   n_prefixes  1 .. W4_MAX_PREFIXES;  table_cols * page_size up to 2^30
+ * The other arguments are those of w4_attn_prefill.  The softmax weights enter the second product as
+ * bf16, their sum in fp32; partial results are fp32 in `work` and joined in a fixed order.
+ */
+typedef struct w4_prefixes {
+    const int32_t *prefix_of, *table, *len;
+    int64_t n_prefixes, table_cols, ld_table;
+} w4_prefixes;
+
+#define W4_MAX_PREFIXES 4096
+
+int w4_attn_shared(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
+                   const w4_kv_cache *cache, const w4_prefixes *prefixes, float scale,
+                   int64_t window, int64_t sinks, void *y, int64_t ldy, int out_dtype, float *lse,
+                   void *work, size_t work_bytes, void *stream);
+size_t w4_attn_shared_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache,
+                                 const w4_prefixes *prefixes, int64_t window, int64_t sinks);
+
+/*
+ * w4_attn_cross -- cross attention: every row sees all kv_len[b] keys of its sequence, which are an
+ * encoder's states (of another length than the rows, and without positions).
+ *   q        bf16 [T][ldq]; the rows q_start[b] .. q_start[b + 1] - 1 belong to sequence b: prompt
+ *            tokens, or the newest tokens of the beams of a request.  q_start NULL: T = n_seqs, one
+ *            row each
+ *   cache    keys and values of the encoder's states; a dense [n_seqs][length][n_kv_heads][head_dim]
+ *            is a cache of pages in ascending order
+ *   the other arguments as for w4_attn_prefill.  A sequence without states gives y = 0, lse = -inf.
+ */
+int w4_attn_cross(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
+                  const w4_kv_cache *cache, float scale, void *y, int64_t ldy, int out_dtype,
+                  float *lse, void *work, size_t work_bytes, void *stream);
+size_t w4_attn_cross_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache);
+
+/*
+ * w4_batch_tables -- the tables of a step, made on the device from the lengths of its requests: pages
+ * for the new tokens, the token rows of each sequence, and the slot of each row.  The results are what
+ * the operators above take, so that a step recorded once replays as sequences begin, grow and end.
+ *   L = kv_len[b],  m = n_new[b],  [begin, end) = spans[b]: the entries of row b of the page table that
+ *   name pages of its own.  (Entries below `begin` are those of a shared prefix, or not used.)
+ *   m >= 0  entries end .. ceil((L + m) / page_size) - 1 get free pages, in the order of the sequences
+ *           and of the entries; kv_len_out[b] = L + m;  spans_out[b] = [begin, end + pages it got)
+ *   m < 0   the sequence ends: its pages are free from the next call on; kv_len_out[b] = 0,
+ *           spans_out[b] = [0, 0).  A sequence that begins sets kv_len and spans itself: 0 and [0, 0),
+ *           or P and [P / page_size, P / page_size) after a prefix of P keys.
+ *   q_start[b + 1] = sum of max(m, 0) up to b;  row t = q_start[b] + i stands at position L + i:
+ *   seqs[t] = b,  positions[t] = L + i,  slots[t] = page * page_size + (L + i) % page_size.
+ * Free pages lie in a ring: ring_state = {head, count, missing}, number k of `count` at place
+ * (head + k) % ring_size.  Pages are taken from its head; pages that come back follow its last one, in
+ * the order of the sequences and of the entries.  Where no page is left the entry becomes -1 (an
+ * append there is dropped), the row's slot -1, and missing_out counts those entries: the step has to
+ * be made again with more free pages, from the same kv_len and spans.  Entries past the table's last
+ * column are neither written nor counted; rows there get slot -1.
+ *   n_new        int32 [n_seqs], values up to 2^30 - 1;  spans, spans_out  int32 [n_seqs][2]
+ *   kv_len, kv_len_out  int32 [n_seqs];   ring_state, ring_state_out  int32 [3]
+ *   page_table   int32 [n_seqs][ld_table], table_cols entries used, in and out
+ *   page_size    a power of two, 1 .. 32768;  table_cols * page_size and n_seqs * table_cols up to 2^30
+ *   ring         int32 [ring_size], in and out.  Pages beyond its size are dropped
+ *   q_start      int32 [n_seqs + 1];  sums beyond T count as T
+ *   slots int64 [T], seqs and positions int32 [T], each may be NULL; rows behind the last sequence's
+ *                get -1 in all three.  T  0 .. W4_MAX_DIM
+ *   An output may be the input of its kind (kv_len_out = kv_len, ...); no other overlap (not checked).
+ */
+int w4_batch_tables(const int32_t *kv_len, const int32_t *n_new, const int32_t *spans,
+                    int64_t n_seqs, int32_t *page_table, int64_t table_cols, int64_t ld_table,
+                    int page_size, int32_t *ring, int64_t ring_size, const int32_t *ring_state,
+                    int64_t T, int32_t *q_start, int64_t *slots, int32_t *seqs,
+                    int32_t *positions, int32_t *kv_len_out, int32_t *spans_out,
+                    int32_t *ring_state_out, void *stream);
+
+/*
  * w4_residual_norm -- the seam between two blocks of a layer: the norm after a block, its gate and
  * residual scale, the residual add, and the norm before the next block, in one pass:
  *   n = x,  or  rms(x, w_post) where w_post is given

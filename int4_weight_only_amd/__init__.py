@@ -23,7 +23,8 @@ __all__ = [
     "W4_ROPE_HALF", "W4_ROPE_INTERLEAVED", "W4_ROPE_PLAIN", "W4_ROPE_LINEAR", "W4_ROPE_NTK",
     "W4_ROPE_YARN", "w4_rope_frequencies", "w4_rope_append", "w4_attn_decode",
     "w4_attn_decode_work_bytes", "w4_attn_prefill", "w4_attn_prefill_work_bytes",
-    "w4_residual_norm",
+    "w4_attn_shared", "w4_attn_shared_work_bytes", "w4_attn_cross", "w4_attn_cross_work_bytes",
+    "w4_batch_tables", "w4_residual_norm",
     "library_path",
 ]
 
@@ -46,6 +47,13 @@ class _KvCache(ctypes.Structure):
                 ("page_table", ctypes.c_void_p), ("n_seqs", ctypes.c_int64),
                 ("table_cols", ctypes.c_int64), ("ld_table", ctypes.c_int64),
                 ("kv_len", ctypes.c_void_p)]
+
+
+class _Prefixes(ctypes.Structure):
+    """w4_prefixes of include/w4.h."""
+    _fields_ = [("prefix_of", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("len", ctypes.c_void_p), ("n_prefixes", ctypes.c_int64),
+                ("table_cols", ctypes.c_int64), ("ld_table", ctypes.c_int64)]
 
 
 class W4Error(RuntimeError):
@@ -90,10 +98,18 @@ def _load(path):
     lib.w4_attn_prefill.argtypes = [p, i64, i64, i32, p, cache] + attn
     lib.w4_attn_prefill_work_bytes.argtypes = [i64, i32, cache, i64, i64]
     lib.w4_attn_prefill_work_bytes.restype = ctypes.c_size_t
+    prefixes = ctypes.POINTER(_Prefixes)
+    lib.w4_attn_shared.argtypes = [p, i64, i64, i32, p, cache, prefixes] + attn
+    lib.w4_attn_shared_work_bytes.argtypes = [i64, i32, cache, prefixes, i64, i64]
+    lib.w4_attn_shared_work_bytes.restype = ctypes.c_size_t
+    lib.w4_attn_cross.argtypes = [p, i64, i64, i32, p, cache, f32] + attn[3:]
+    lib.w4_attn_cross_work_bytes.argtypes = [i64, i32, cache]
+    lib.w4_attn_cross_work_bytes.restype = ctypes.c_size_t
+    lib.w4_batch_tables.argtypes = [p, p, p, i64, p, i64, i64, i32, p, i64, p, i64] + [p] * 8
     lib.w4_residual_norm.argtypes = [p, i64, p, i64, i32, i64, i64, p, p, f32, p, i64, f32, f32,
                                      p, i64, p, i64, p]
     for f in ("w4_rope_frequencies", "w4_rope_append", "w4_attn_decode", "w4_attn_prefill",
-              "w4_residual_norm"):
+              "w4_attn_shared", "w4_attn_cross", "w4_batch_tables", "w4_residual_norm"):
         getattr(lib, f).restype = i32
     for f in ("w4_packed_layout", "w4_pack", "w4_qat_repack", "w4_gptq_hessian", "w4_gptq_factor",
               "w4_gptq_quantize", "w4_gptq_quantize_noalloc", "w4_gemv", "w4_gemv_ws",
@@ -654,6 +670,132 @@ def w4_attn_prefill_work_bytes(T, n_heads, k_cache, v_cache, page_table, kv_len,
     """Bytes of workspace w4_attn_prefill needs for these sizes (0: none)."""
     cache = _kv_cache(k_cache, v_cache, page_table, kv_len, k_cache.device)
     return int(_lib.w4_attn_prefill_work_bytes(T, n_heads, ctypes.byref(cache), window, sinks))
+
+
+def _prefixes(prefix_of, prefix_table, prefix_len, n_seqs, dev):
+    """The ABI's view of the prefixes of n_seqs sequences."""
+    _need(prefix_of, "prefix_of", torch.int32, dev, 1)
+    _need(prefix_table, "prefix_table", torch.int32, dev, 2)
+    _need(prefix_len, "prefix_len", torch.int32, dev, 1)
+    n, cols = prefix_table.shape
+    if prefix_of.shape[0] != n_seqs:
+        raise ValueError(f"prefix_of must have {n_seqs} elements")
+    if prefix_len.shape[0] != n:
+        raise ValueError(f"prefix_len must have {n} elements")
+    return _Prefixes(prefix_of.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(), n, cols,
+                     prefix_table.stride(0) if n > 1 else cols)
+
+
+def _rows_attention(name, q, cache, prefixes, q_start, scale, mask, out_dtype, out, want_lse, work):
+    """w4_attn_shared, or w4_attn_cross where there are no prefixes (and no mask)."""
+    dev = q.device
+    T, width = q.shape
+    D = cache.head_dim
+    if width % D != 0:
+        raise ValueError(f"q has {width} columns, not a multiple of head_dim={D}")
+    if q_start is not None:
+        _need_q_start(q_start, cache.n_seqs, dev)
+    elif T != cache.n_seqs:
+        raise ValueError(f"q must have one row for each of {cache.n_seqs} sequences")
+    n_heads = width // D
+    views = [ctypes.byref(x) for x in (cache, prefixes) if x is not None]
+    need = getattr(_lib, name + "_work_bytes")(T, n_heads, *views, *mask)
+    if work is None:
+        if need:
+            work = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        _need(work, "work", torch.uint8, dev, 1)
+    out = _out(out, T, width, torch.float32 if out_dtype == W4_OUT_F32 else torch.bfloat16, dev)
+    lse = torch.empty((T, n_heads), dtype=torch.float32, device=dev) if want_lse else None
+    _check(name, getattr(_lib, name)(
+        q.data_ptr(), T, q.stride(0) if T > 1 else width, n_heads, _ptr(q_start), *views,
+        D ** -0.5 if scale is None else scale, *mask, out.data_ptr(),
+        out.stride(0) if T > 1 else width, out_dtype, _ptr(lse), _ptr(work),
+        0 if work is None else work.numel(), _stream(dev)))
+    return (out, lse) if want_lse else out
+
+
+def w4_attn_shared(q, k_cache, v_cache, page_table, kv_len, prefix_of, prefix_table, prefix_len,
+                   q_start=None, scale=None, window=0, sinks=0, out_dtype=W4_OUT_BF16, out=None,
+                   want_lse=False, work=None):
+    """w4_attn_decode (q_start None) or w4_attn_prefill of sequences that share prefixes, each of
+    which is read once for all of them.  prefix_of int32 [n_seqs]: the prefix of each sequence (-1:
+    none); prefix_table int32 [n_prefixes][cols] and prefix_len int32 [n_prefixes]: its pages and
+    keys.  kv_len counts the prefix; page_table's entries below it are not read.  work: a uint8
+    tensor of at least w4_attn_shared_work_bytes bytes (None: one is allocated where needed)."""
+    _need(q, "q", torch.bfloat16, dim=2)
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, q.device)
+    prefixes = _prefixes(prefix_of, prefix_table, prefix_len, cache.n_seqs, q.device)
+    return _rows_attention("w4_attn_shared", q, cache, prefixes, q_start, scale, (window, sinks),
+                           out_dtype, out, want_lse, work)
+
+
+def w4_attn_cross(q, k_cache, v_cache, page_table, kv_len, q_start=None, scale=None,
+                  out_dtype=W4_OUT_BF16, out=None, want_lse=False, work=None):
+    """Cross attention: every row sees all kv_len keys of its sequence.  q bf16 [T][n_heads *
+    head_dim], the rows q_start[b] .. q_start[b + 1] - 1 being those of sequence b (None: one row
+    each); the cache holds the keys and values of an encoder's states.  Otherwise as
+    w4_attn_prefill; work: at least w4_attn_cross_work_bytes bytes."""
+    _need(q, "q", torch.bfloat16, dim=2)
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, q.device)
+    return _rows_attention("w4_attn_cross", q, cache, None, q_start, scale, (), out_dtype, out,
+                           want_lse, work)
+
+
+def w4_attn_shared_work_bytes(T, n_heads, k_cache, v_cache, page_table, kv_len, prefix_of,
+                              prefix_table, prefix_len, window=0, sinks=0):
+    """Bytes of workspace w4_attn_shared needs for these sizes (0: none)."""
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, k_cache.device)
+    prefixes = _prefixes(prefix_of, prefix_table, prefix_len, cache.n_seqs, k_cache.device)
+    return int(_lib.w4_attn_shared_work_bytes(T, n_heads, ctypes.byref(cache),
+                                              ctypes.byref(prefixes), window, sinks))
+
+
+def w4_attn_cross_work_bytes(T, n_heads, k_cache, v_cache, page_table, kv_len):
+    """Bytes of workspace w4_attn_cross needs for these sizes (0: none)."""
+    cache = _kv_cache(k_cache, v_cache, page_table, kv_len, k_cache.device)
+    return int(_lib.w4_attn_cross_work_bytes(T, n_heads, ctypes.byref(cache)))
+
+
+def w4_batch_tables(kv_len, n_new, spans, page_table, page_size, ring, ring_state, T,
+                    in_place=False):
+    """The tables of a step from the lengths of its requests, on the GPU: free pages of the ring for
+    the n_new tokens of each sequence (below 0: it ends and its pages come back), written to
+    page_table and ring.  kv_len, n_new int32 [n_seqs]; spans int32 [n_seqs][2], the entries of its
+    page_table row that are each sequence's own; ring int32 [pages], ring_state int32 [3] (head,
+    count, missing).  T: token rows of the step (those behind the last sequence's get -1).
+
+    Returns (q_start int32 [n_seqs + 1], slots int64 [T], seqs int32 [T], positions int32 [T],
+    kv_len, spans, ring_state), the last three new tensors, or with in_place those given."""
+    _need(kv_len, "kv_len", torch.int32, dim=1)
+    dev = kv_len.device
+    _need(n_new, "n_new", torch.int32, dev, 1)
+    _need(spans, "spans", torch.int32, dev, 2)
+    _need(page_table, "page_table", torch.int32, dev, 2)
+    _need(ring, "ring", torch.int32, dev, 1)
+    _need(ring_state, "ring_state", torch.int32, dev, 1)
+    n_seqs, cols = page_table.shape
+    if kv_len.shape[0] != n_seqs or n_new.shape[0] != n_seqs:
+        raise ValueError(f"kv_len and n_new must have {n_seqs} elements")
+    if tuple(spans.shape) != (n_seqs, 2) or not spans.is_contiguous():
+        raise ValueError(f"spans must be contiguous [{n_seqs}][2]")
+    if ring_state.shape[0] != 3:
+        raise ValueError("ring_state must have 3 elements")
+    q_start = torch.empty(n_seqs + 1, dtype=torch.int32, device=dev)
+    slots = torch.empty(T, dtype=torch.int64, device=dev)
+    seqs, positions = torch.empty((2, T), dtype=torch.int32, device=dev).unbind()
+    if not in_place:
+        kv_out = torch.empty(n_seqs, dtype=torch.int32, device=dev)
+        spans_out = torch.empty((n_seqs, 2), dtype=torch.int32, device=dev)
+        state_out = torch.empty(3, dtype=torch.int32, device=dev)
+    else:
+        kv_out, spans_out, state_out = kv_len, spans, ring_state
+    _check("w4_batch_tables", _lib.w4_batch_tables(
+        kv_len.data_ptr(), n_new.data_ptr(), spans.data_ptr(), n_seqs, page_table.data_ptr(), cols,
+        page_table.stride(0) if n_seqs > 1 else cols, page_size, ring.data_ptr(), ring.shape[0],
+        ring_state.data_ptr(), T, q_start.data_ptr(), _ptr(slots), _ptr(seqs), _ptr(positions),
+        kv_out.data_ptr(), spans_out.data_ptr(), state_out.data_ptr(), _stream(dev)))
+    return q_start, slots, seqs, positions, kv_out, spans_out, state_out
 
 
 def w4_residual_norm(x, residual, w_pre, w_post=None, gate=None, alpha=1.0, eps=1e-6,

@@ -1,6 +1,6 @@
 // abi_layer.hip -- the extern "C" entry points of the operators between a decoder layer's linears
-// (rotary positions with the cache append, attention over the paged cache, the residual norm):
-// host-side argument validation and dispatch.  The contract of every entry point is stated in
+// (rotary positions with the cache append, the tables of a step, attention over the paged cache, the
+// residual norm): host-side argument validation and dispatch.  The contract of every entry point is stated in
 // include/w4.h; nothing here allocates device memory or synchronizes.
 #include <hip/hip_runtime.h>
 
@@ -127,6 +127,23 @@ int check_attn(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int
     a->out_f32 = out_dtype == W4_OUT_F32;
     a->lse = lse;
     a->work = work;
+    return W4_OK;
+}
+
+int check_prefixes(const w4_prefixes *p, const w4::KvView &c, w4::Prefixes *x) {
+    if (!p || !p->prefix_of || !p->table || !p->len) return W4_ERR_NULL;
+    if (p->n_prefixes < 1 || p->table_cols < 1 || p->ld_table < p->table_cols) return W4_ERR_SHAPE;
+    if (p->n_prefixes > W4_MAX_PREFIXES || p->ld_table > INT32_MAX ||
+        p->table_cols > (1 << 30) >> c.page_shift)
+        return W4_ERR_RANGE;
+    if (!aligned(p->prefix_of, 4) || !aligned(p->table, 4) || !aligned(p->len, 4))
+        return W4_ERR_ALIGN;
+    x->of = p->prefix_of;
+    x->table = p->table;
+    x->len = p->len;
+    x->ld_table = p->ld_table;
+    x->n = static_cast<int32_t>(p->n_prefixes);
+    x->capacity = static_cast<int32_t>(p->table_cols << c.page_shift);
     return W4_OK;
 }
 
@@ -258,6 +275,116 @@ int w4_attn_prefill(const uint16_t *q, int64_t T, int64_t ldq, int n_heads,
         return st;
     return guarded(
         [&] { return w4::launch_attn_prefill(a, view, static_cast<hipStream_t>(stream)); });
+}
+
+size_t w4_attn_shared_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache,
+                                 const w4_prefixes *prefixes, int64_t window, int64_t sinks) {
+    w4::KvView view;
+    w4::Prefixes x;
+    w4::AttnArgs a{};
+    if (T < 1 || T > W4_MAX_DIM || check_cache(cache, n_heads, &view) ||
+        check_prefixes(prefixes, view, &x) || check_mask(window, sinks, view, &a) ||
+        !w4::attn_shared_supported(T, n_heads, view, x, a.window, a.sinks))
+        return 0;
+    return w4::attn_shared_work_bytes(T, n_heads, view, x, a.window, a.sinks);
+}
+
+int w4_attn_shared(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
+                   const w4_kv_cache *cache, const w4_prefixes *prefixes, float scale,
+                   int64_t window, int64_t sinks, void *y, int64_t ldy, int out_dtype, float *lse,
+                   void *work, size_t work_bytes, void *stream) {
+    w4::KvView view;
+    w4::Prefixes x;
+    w4::AttnArgs a{};
+    if (int st = check_attn(q, T, ldq, n_heads, q_start, cache, scale, window, sinks, y, ldy,
+                            out_dtype, lse, work, &view, &a))
+        return st;
+    if (int st = check_prefixes(prefixes, view, &x)) return st;
+    if (!q_start && T != view.n_seqs) return W4_ERR_SHAPE;
+    if (!w4::attn_shared_supported(T, n_heads, view, x, a.window, a.sinks)) return W4_ERR_RANGE;
+    if (int st = check_work(w4::attn_shared_work_bytes(T, n_heads, view, x, a.window, a.sinks),
+                            work, work_bytes))
+        return st;
+    return guarded(
+        [&] { return w4::launch_attn_shared(a, view, x, static_cast<hipStream_t>(stream)); });
+}
+
+size_t w4_attn_cross_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache) {
+    w4::KvView view;
+    if (T < 1 || T > W4_MAX_DIM || check_cache(cache, n_heads, &view) ||
+        !w4::attn_cross_supported(T, n_heads, view))
+        return 0;
+    return w4::attn_cross_work_bytes(T, n_heads, view);
+}
+
+int w4_attn_cross(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
+                  const w4_kv_cache *cache, float scale, void *y, int64_t ldy, int out_dtype,
+                  float *lse, void *work, size_t work_bytes, void *stream) {
+    w4::KvView view;
+    w4::AttnArgs a{};
+    if (int st = check_attn(q, T, ldq, n_heads, q_start, cache, scale, 0, 0, y, ldy, out_dtype, lse,
+                            work, &view, &a))
+        return st;
+    if (!q_start && T != view.n_seqs) return W4_ERR_SHAPE;
+    if (!w4::attn_cross_supported(T, n_heads, view)) return W4_ERR_RANGE;
+    if (int st = check_work(w4::attn_cross_work_bytes(T, n_heads, view), work, work_bytes))
+        return st;
+    return guarded(
+        [&] { return w4::launch_attn_cross(a, view, static_cast<hipStream_t>(stream)); });
+}
+
+int w4_batch_tables(const int32_t *kv_len, const int32_t *n_new, const int32_t *spans,
+                    int64_t n_seqs, int32_t *page_table, int64_t table_cols, int64_t ld_table,
+                    int page_size, int32_t *ring, int64_t ring_size, const int32_t *ring_state,
+                    int64_t T, int32_t *q_start, int64_t *slots, int32_t *seqs,
+                    int32_t *positions, int32_t *kv_len_out, int32_t *spans_out,
+                    int32_t *ring_state_out, void *stream) {
+    if (!kv_len || !n_new || !spans || !page_table || !ring || !ring_state || !q_start ||
+        !kv_len_out || !spans_out || !ring_state_out)
+        return W4_ERR_NULL;
+    if (n_seqs < 1 || table_cols < 1 || ld_table < table_cols || page_size < 1 || ring_size < 1 ||
+        T < 0)
+        return W4_ERR_SHAPE;
+    if (page_size > 32768 || n_seqs > W4_MAX_DIM || T > W4_MAX_DIM || ld_table > INT32_MAX ||
+        ring_size > INT32_MAX || table_cols > (1 << 30) / page_size ||
+        n_seqs > (1 << 30) / table_cols)
+        return W4_ERR_RANGE;
+    if ((page_size & (page_size - 1)) != 0) return W4_ERR_UNSUPPORTED;
+    for (const void *p : {static_cast<const void *>(kv_len), static_cast<const void *>(n_new),
+                          static_cast<const void *>(spans), static_cast<const void *>(page_table),
+                          static_cast<const void *>(ring), static_cast<const void *>(ring_state),
+                          static_cast<const void *>(q_start), static_cast<const void *>(seqs),
+                          static_cast<const void *>(positions),
+                          static_cast<const void *>(kv_len_out),
+                          static_cast<const void *>(spans_out),
+                          static_cast<const void *>(ring_state_out)})
+        if (!aligned(p, 4)) return W4_ERR_ALIGN;
+    if (!aligned(slots, 8)) return W4_ERR_ALIGN;
+    w4::TablesArgs a{};
+    a.kv_len = kv_len;
+    a.n_new = n_new;
+    a.spans = spans;
+    a.page_table = page_table;
+    a.ring = ring;
+    a.ring_state = ring_state;
+    a.q_start = q_start;
+    a.slots = slots;
+    a.seqs = seqs;
+    a.positions = positions;
+    a.kv_len_out = kv_len_out;
+    a.spans_out = spans_out;
+    a.ring_state_out = ring_state_out;
+    a.ld_table = ld_table;
+    a.n_seqs = static_cast<int32_t>(n_seqs);
+    a.table_cols = static_cast<int32_t>(table_cols);
+    a.page_shift = __builtin_ctz(static_cast<unsigned>(page_size));
+    a.ring_size = static_cast<int32_t>(ring_size);
+    a.T = static_cast<int32_t>(T);
+    const bool in_place =
+        kv_len == kv_len_out || spans == spans_out || ring_state == ring_state_out;
+    return guarded([&] {
+        return w4::launch_batch_tables(a, in_place, static_cast<hipStream_t>(stream));
+    });
 }
 
 int w4_residual_norm(const uint16_t *x, int64_t ldx, const void *r, int64_t ldr, int r_dtype,

@@ -20,6 +20,15 @@ struct KvView {
     int32_t n_kv, head_dim, n_seqs;
 };
 
+// Checked w4_prefixes: shared prefixes of the sequences of a cache.
+struct Prefixes {
+    const int32_t *of;     // [n_seqs], a prefix, or anything outside [0, n) for none
+    const int32_t *table;  // [n][ld_table], `capacity` positions each
+    const int32_t *len;    // [n]
+    int64_t ld_table;
+    int32_t n, capacity;
+};
+
 #if defined(__HIPCC__)
 
 // An element of an array that nothing writes while the kernel runs (page tables, lengths): a scalar
@@ -47,6 +56,19 @@ __device__ __forceinline__ int64_t kv_offset(const KvView &c, const int32_t *row
                                              int head) {
     return static_cast<int64_t>(kv_page(c, row, pos)) * c.page_stride +
            static_cast<int64_t>((pos & c.page_mask) * c.slot_stride + head * c.head_stride);
+}
+
+// Keys of prefix g; a length outside what its table can hold is cut to it.
+__device__ __forceinline__ int prefix_length(const Prefixes &x, int g) {
+    const int n = read_const(x.len + g);
+    return n < 0 ? 0 : (n > x.capacity ? x.capacity : n);
+}
+// Positions of sequence b that lie in its prefix, and that prefix's table row (as it was without one).
+__device__ __forceinline__ int prefix_of_seq(const Prefixes &x, int b, const int32_t **row) {
+    const int g = read_const(x.of + b);
+    if (g < 0 || g >= x.n) return 0;
+    *row = x.table + g * x.ld_table;
+    return prefix_length(x, g);
 }
 
 // Where token row t stands: its sequence, that sequence's keys, and its position (below 0: it sees

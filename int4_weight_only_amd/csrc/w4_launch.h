@@ -164,6 +164,32 @@ hipError_t launch_attn_decode(const AttnArgs &a, const KvView &cache, hipStream_
 size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &cache, int window, int sinks);
 hipError_t launch_attn_prefill(const AttnArgs &a, const KvView &cache, hipStream_t stream);
 
+// Attention of sequences that share prefixes, and cross attention (attn_shared.hip). Without q_start
+// a.T is the number of sequences.
+bool attn_shared_supported(int64_t T, int n_heads, const KvView &cache, const Prefixes &prefixes,
+                           int window, int sinks);
+size_t attn_shared_work_bytes(int64_t T, int n_heads, const KvView &cache,
+                              const Prefixes &prefixes, int window, int sinks);
+hipError_t launch_attn_shared(const AttnArgs &a, const KvView &cache, const Prefixes &prefixes,
+                              hipStream_t stream);
+bool attn_cross_supported(int64_t T, int n_heads, const KvView &cache);
+size_t attn_cross_work_bytes(int64_t T, int n_heads, const KvView &cache);
+hipError_t launch_attn_cross(const AttnArgs &a, const KvView &cache, hipStream_t stream);
+
+// Tables, lengths and slots of a step (tables.hip). slots, seqs and positions may be NULL; in_place:
+// an output is the input of its kind.
+struct TablesArgs {
+    const int32_t *kv_len, *n_new, *spans;
+    int32_t *page_table, *ring;
+    const int32_t *ring_state;
+    int32_t *q_start;
+    int64_t *slots;
+    int32_t *seqs, *positions, *kv_len_out, *spans_out, *ring_state_out;
+    int64_t ld_table;
+    int32_t n_seqs, table_cols, page_shift, ring_size, T;
+};
+hipError_t launch_batch_tables(const TablesArgs &a, bool in_place, hipStream_t stream);
+
 // The residual norm (norm.hip); pointers checked, r and r_out of the type r_f32 says.
 struct NormArgs {
     const uint16_t *x;
