@@ -311,10 +311,14 @@ int w4_attn_shared(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const
 
 size_t w4_attn_cross_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache) {
     w4::KvView view;
-    if (T < 1 || T > W4_MAX_DIM || check_cache(cache, n_heads, &view) ||
-        !w4::attn_cross_supported(T, n_heads, view))
-        return 0;
-    return w4::attn_cross_work_bytes(T, n_heads, view);
+    if (T < 1 || T > W4_MAX_DIM || check_cache(cache, n_heads, &view)) return 0;
+    size_t need = 0;  // the larger of the forms that T may stand for
+    for (const bool single : {false, true})
+        if ((!single || T == view.n_seqs) && w4::attn_cross_supported(T, n_heads, view, single)) {
+            const size_t n = w4::attn_cross_work_bytes(T, n_heads, view, single);
+            need = n > need ? n : need;
+        }
+    return need;
 }
 
 int w4_attn_cross(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
@@ -326,8 +330,9 @@ int w4_attn_cross(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const 
                             work, &view, &a))
         return st;
     if (!q_start && T != view.n_seqs) return W4_ERR_SHAPE;
-    if (!w4::attn_cross_supported(T, n_heads, view)) return W4_ERR_RANGE;
-    if (int st = check_work(w4::attn_cross_work_bytes(T, n_heads, view), work, work_bytes))
+    if (!w4::attn_cross_supported(T, n_heads, view, !q_start)) return W4_ERR_RANGE;
+    if (int st = check_work(w4::attn_cross_work_bytes(T, n_heads, view, !q_start), work,
+                            work_bytes))
         return st;
     return guarded(
         [&] { return w4::launch_attn_cross(a, view, static_cast<hipStream_t>(stream)); });

@@ -65,14 +65,4 @@ hipError_t launch_attn_shared(const AttnArgs &a, const KvView &c, const Prefixes
                        dim3(kWaves * 64), 0, stream, a, c, x);
     return hipGetLastError();
 }
-bool attn_cross_supported(int64_t T, int n_heads, const KvView &) {
-    return T * n_heads <= static_cast<int64_t>(kMaxThreads) / (kWaves * 64);
-}
-size_t attn_cross_work_bytes(int64_t, int, const KvView &) { return 0; }
-hipError_t launch_attn_cross(const AttnArgs &a, const KvView &c, hipStream_t stream) {
-    hipLaunchKernelGGL(attn_rows_kernel<true>, dim3(static_cast<unsigned>(a.T * a.n_heads)),
-                       dim3(kWaves * 64), 0, stream, a, c, Prefixes{});
-    return hipGetLastError();
-}
-
 }  // namespace w4

@@ -164,16 +164,17 @@ hipError_t launch_attn_decode(const AttnArgs &a, const KvView &cache, hipStream_
 size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &cache, int window, int sinks);
 hipError_t launch_attn_prefill(const AttnArgs &a, const KvView &cache, hipStream_t stream);
 
-// Attention of sequences that share prefixes, and cross attention (attn_shared.hip). Without q_start
-// a.T is the number of sequences.
+// Attention of sequences that share prefixes, and cross attention (attn_shared.hip, attn_prefill.hip).
+// Without q_start a.T is the number of sequences.
 bool attn_shared_supported(int64_t T, int n_heads, const KvView &cache, const Prefixes &prefixes,
                            int window, int sinks);
 size_t attn_shared_work_bytes(int64_t T, int n_heads, const KvView &cache,
                               const Prefixes &prefixes, int window, int sinks);
 hipError_t launch_attn_shared(const AttnArgs &a, const KvView &cache, const Prefixes &prefixes,
                               hipStream_t stream);
-bool attn_cross_supported(int64_t T, int n_heads, const KvView &cache);
-size_t attn_cross_work_bytes(int64_t T, int n_heads, const KvView &cache);
+// (single: without q_start)
+bool attn_cross_supported(int64_t T, int n_heads, const KvView &cache, bool single);
+size_t attn_cross_work_bytes(int64_t T, int n_heads, const KvView &cache, bool single);
 hipError_t launch_attn_cross(const AttnArgs &a, const KvView &cache, hipStream_t stream);
 
 // Tables, lengths and slots of a step (tables.hip). slots, seqs and positions may be NULL; in_place:
