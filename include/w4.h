@@ -480,7 +480,9 @@ size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cac
  *   len         int32 [n_prefixes]: keys of each prefix; below 0 as 0, above table_cols * page_size
  *               as that
  *   n_prefixes  1 .. W4_MAX_PREFIXES;  table_cols * page_size up to 2^30
- * The other arguments are those of w4_attn_prefill.  The softmax weights enter the second product as
+ * The other arguments are those of w4_attn_prefill.  Limits (W4_ERR_RANGE): those of w4_attn_prefill,
+ * with twice the rows, and for U = T * n_heads / n_kv_heads / 64 + 2 n_seqs, U times the tiles of 64
+ * keys (32 for head_dim > 128) in table_cols pages of either table below 2^31.  The softmax weights enter the second product as
  * bf16, their sum in fp32; partial results are fp32 in `work` and joined in a fixed order.
  */
 typedef struct w4_prefixes {
@@ -488,7 +490,7 @@ typedef struct w4_prefixes {
     int64_t n_prefixes, table_cols, ld_table;
 } w4_prefixes;
 
-#define W4_MAX_PREFIXES 4096
+#define W4_MAX_PREFIXES 2048
 
 int w4_attn_shared(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
                    const w4_kv_cache *cache, const w4_prefixes *prefixes, float scale,

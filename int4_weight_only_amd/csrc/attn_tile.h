@@ -44,7 +44,9 @@ struct TileRows {
     const int32_t *first_table;
     int cut;
     bool from_cut, to_cut;
-    int64_t slot;  // (Rows' own: where the partial sums go)
+    // (of Rows with two tables: rows of a prefix, rows written as they are, place of partial sums)
+    bool of_prefix, direct;
+    int extra;
 };
 
 // The key tiles that the rows of a workgroup see: those of the sinks, then those from `lo` on. Where
@@ -265,10 +267,11 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
     const auto span_at = [&](int i) { return (i * NW + wid) * kSpan; };
     // (of a tile whose table holds the keys begin .. end)
     const auto all_seen = [&](int k0, int begin, int end) {  // each key by some row of the block
-        return (k0 >= begin) & (k0 + KT - 1 <= end) & ((k0 >= lo) | (k0 + KT - 1 < sinks_end));
+        return (!TABLES | (k0 >= begin)) & (k0 + KT - 1 <= end) &
+               ((k0 >= lo) | (k0 + KT - 1 < sinks_end));
     };
     const auto visible = [&](int p, int begin, int end) {
-        return (p >= begin) & (p <= end) & ((p >= lo) | (p < sinks_end));
+        return (!TABLES | (p >= begin)) & (p <= end) & ((p >= lo) | (p < sinks_end));
     };
     // a key that is seen, among the n from s0 on if any is
     const auto safe_of = [&](int s0, int n, int begin, int end) {
@@ -324,7 +327,8 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
         if constexpr (PAGES == kTilePages) {
             w.base[0] = page_offset(entry[0]) +
                         static_cast<int64_t>((k0 & c.page_mask) * c.slot_stride);
-            const int first = max(k0, begin), safe = first < sinks_end ? first : max(first, lo);
+            const int first = TABLES ? max(k0, begin) : k0;
+            const int safe = first < sinks_end ? first : max(first, lo);
             const uint32_t other = (safe - k0) * c.slot_stride;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
@@ -560,6 +564,7 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
     const auto write_row = [&]() __attribute__((always_inline)) {
         l += other_half(l);
         if (!t.live || half != 0) return;
+        if constexpr (TABLES) Rows::write_record(args, t);
         if (Rows::is_partial(args, t))
             Rows::write_sums(args, t, M, l);
         else if (a.lse)
