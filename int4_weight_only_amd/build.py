@@ -15,7 +15,7 @@ LIB = os.path.join(HERE, "libw4.so")
 SOURCES = ["abi.hip", "codec.hip", "decode.hip", "decode_i8.hip", "decode_mfma.hip", "decode_split.hip",
            "decode_stream.hip", "decode_w4a8_mfma.hip", "gemm.hip", "gemm_w4a8.hip", "qat_repack.hip",
            "gptq.hip", "abi_layer.hip", "rope.hip", "norm.hip", "attn_decode.hip", "attn_prefill.hip",
-           "attn_shared.hip", "tables.hip"]
+           "attn_units.hip", "tables.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

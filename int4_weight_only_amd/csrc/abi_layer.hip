@@ -284,9 +284,9 @@ size_t w4_attn_shared_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cach
     w4::AttnArgs a{};
     if (T < 1 || T > W4_MAX_DIM || check_cache(cache, n_heads, &view) ||
         check_prefixes(prefixes, view, &x) || check_mask(window, sinks, view, &a) ||
-        !w4::attn_shared_supported(T, n_heads, view, x, a.window, a.sinks))
+        !w4::attn_shared_supported(T, n_heads, view, x))
         return 0;
-    return w4::attn_shared_work_bytes(T, n_heads, view, x, a.window, a.sinks);
+    return w4::attn_shared_work_bytes(T, n_heads, view);
 }
 
 int w4_attn_shared(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
@@ -301,9 +301,8 @@ int w4_attn_shared(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const
         return st;
     if (int st = check_prefixes(prefixes, view, &x)) return st;
     if (!q_start && T != view.n_seqs) return W4_ERR_SHAPE;
-    if (!w4::attn_shared_supported(T, n_heads, view, x, a.window, a.sinks)) return W4_ERR_RANGE;
-    if (int st = check_work(w4::attn_shared_work_bytes(T, n_heads, view, x, a.window, a.sinks),
-                            work, work_bytes))
+    if (!w4::attn_shared_supported(T, n_heads, view, x)) return W4_ERR_RANGE;
+    if (int st = check_work(w4::attn_shared_work_bytes(T, n_heads, view), work, work_bytes))
         return st;
     return guarded(
         [&] { return w4::launch_attn_shared(a, view, x, static_cast<hipStream_t>(stream)); });

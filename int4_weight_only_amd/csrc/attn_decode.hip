@@ -1,44 +1,27 @@
 // attn_decode.hip -- attention of one new token per sequence over the paged cache.
 //
-// One pass over the keys and values of a sequence (w4_attn_decode), bound by reading them: 1 flop
-// per byte and query head (1.5 with the weights in two parts, below). The G = n_heads / n_kv query
-// heads of a key-value head are the columns of one 16-wide matrix-core tile, so that a key is read
-// once for up to 16 of them (more heads read it once per 16: 32 heads over 1, 32 x 4096 keys, 26
-// us).
-//
-//   S^T[key][head] = K Q^T   on v_mfma_f32_16x16x32_bf16; a lane's 16 bytes of a key row are the
-//                            operand as they come from memory
-//   O^T[d][head]  += V^T P^T V through LDS and its transposed read; P^T is, register for register,
-//                            the operand: V's rows follow the key order the first product left
-// P enters the second product as the sum of two bf16 values (16 bits of each weight): the matrix
-// cores have time to spare here.
+// One pass over the keys and values of a sequence (w4_attn_decode), by attn_narrow.h: a unit's rows
+// are the G = n_heads / n_kv query heads of a key-value head, up to 16 of them (more heads read the
+// keys once per 16: 32 heads over 1, 32 x 4096 keys, 26 us).
 //
 // A sequence's visible keys (its sinks, then its window; all without a window) are cut into tiles
 // of 32 keys. Every unit (sequence, key-value head, 16 query heads) is cut into equal shares of at
 // most `per` tiles, a workgroup each, `per` being such that the shares of all sequences together
 // fill the card once: ragged lengths leave no compute unit idle. In a workgroup each of the four
-// waves takes every fourth tile on its own (no barrier in the loop, the next tile's loads in
-// flight), and the waves join in LDS. The shares of a unit that was cut meet in the caller's
-// workspace, and a second kernel joins them in order.
+// waves takes every fourth tile, and the waves join in LDS. The shares of a unit that was cut meet
+// in the caller's workspace, and a second kernel joins them in order.
 //
 // 28 heads over 4 of 128: 4 sequences of up to 131072 keys 185 us (5.5 TB/s of keys and values; a
 // large copy reaches 5.0 to 5.5, an elementwise pass 6.3), 32 of up to 8192 63 us (4.4 TB/s). One
 // sequence of 4097 keys takes 11.3 us: nothing but waits for memory, one after the other (page,
 // keys, partial results), and two launches (7.2 and 4.2 us).
-#include <type_traits>
-
-#include "attn_device.h"
+#include "attn_narrow.h"
 
 namespace w4 {
 
 namespace {
 
-constexpr int kTile = 32;   // keys of a tile
-constexpr int kWaves = 4;
-constexpr int kRows = 16;   // query heads of a workgroup
-constexpr int kSlack = 8;   // log2 of how far a weight may pass 1 before the sums are rescaled
-// Values that are not finite, counted over a tile's keys: bf16 64 for minus infinity, 4096 for NaN.
-constexpr uint32_t kMinus = 0x4280u, kNan = 0x4580u;
+constexpr int kTile = kNarrowTile, kWaves = kNarrowWaves, kRows = kNarrowRows;
 
 // The visible keys of a sequence, as tiles.
 struct Keys {
@@ -140,9 +123,27 @@ __device__ __forceinline__ void write_empty(const AttnArgs &a, const KvView &c, 
             a.lse[static_cast<int64_t>(b) * a.n_heads + h] = -INFINITY;
 }
 
-// PAGE16: pages of 16 slots and more, so that 16 aligned keys lie in one page, whose address is
-// looked up a tile ahead, once for all lanes. (Else each row looks up its own: 32 x 8192 keys,
-// 16 heads over 4 of 256, window 1024, 62 us for 33; one of 4097, 28 over 4 of 128, 11.8 for 11.0.)
+// A unit as a wave goes through it (narrow_wave).
+struct DecodeUnit {
+    const AttnArgs &a;
+    Keys keys;
+    const int32_t *table;
+    int b, head, head0, n_rows, D;
+    __device__ __forceinline__ const uint16_t *query() const {
+        const int r = min(static_cast<int>(threadIdx.x & 15), n_rows - 1);
+        return a.q + b * a.ldq + static_cast<int64_t>(head0 + r) * D;
+    }
+    __device__ __forceinline__ int start(int t) const { return keys.start(t); }
+    __device__ __forceinline__ bool visible(int p) const {
+        return (p <= keys.last) & ((p >= keys.lo) | (p < a.sinks));
+    }
+    __device__ __forceinline__ bool sees(int p) const { return visible(p); }
+    __device__ __forceinline__ int safe_key(int s0) const {  // (the newest key if there is none)
+        if (s0 < a.sinks && s0 < keys.lo) return s0;
+        return s0 > keys.last || s0 + 15 < keys.lo ? keys.last : max(s0, keys.lo);
+    }
+};
+
 // Registers: sums, queries and a tile of keys and values take 112 of them at 128 dims (3 waves a
 // SIMD; 4 spill: decode of 4 x 131072 keys 292 us for 188) and 224 at 256 dims (one wave a SIMD; 2
 // spill: 32 x 8192 keys, window 1024, 54 us for 34).
@@ -150,23 +151,12 @@ template <int DP, bool PAGE16>
 __global__ void __launch_bounds__(kWaves * 64)
 __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode_kernel(
     AttnArgs a, KvView c, Plan plan) {
-    constexpr int KS = DP / 32;      // steps of the first product
-    constexpr int DT = DP / 16;      // tiles of the second
-    constexpr int kChunks = DP / 8;  // 16-byte chunks of a row
-    constexpr int kVRows = 64 / kChunks;       // rows a wave's load instruction covers
-    constexpr int kVLoads = kTile / kVRows;
-    // elements from row to row of a value tile: a transposed read takes 32 bytes of 4 consecutive
-    // rows at once, which the gap puts 32 bytes further each in the 64 banks
-    constexpr int kRow = DP + 16;
     // per wave: the value tile, 32 rows of bf16; after the loop its sums, 16 rows of fp32
-    __shared__ __attribute__((aligned(16))) uint16_t sv[kWaves][kTile * kRow];
+    __shared__ __attribute__((aligned(16))) uint16_t sv[kWaves][kNarrowElements<DP>];
     __shared__ float sm[kWaves][kRows], sl[kWaves][kRows];
 
-    const int wid = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int G = a.n_heads / c.n_kv, D = c.head_dim;
     const int row_tiles = (G + kRows - 1) / kRows;
-    const float cs = a.scale * kLog2e;
-    uint16_t *my_v = sv[wid];
 
     // A sequence without keys has no share: its rows are written by the group of its number.
     for (int e = blockIdx.x; e < c.n_seqs; e += gridDim.x)
@@ -199,292 +189,53 @@ __attribute__((amdgpu_waves_per_eu(DP > 128 ? 1 : DP > 64 ? 3 : 4))) attn_decode
     unit = uniform(unit);
     t0 = uniform(t0);
     t1 = uniform(t1);
-    {
-        const int tid = threadIdx.x, lane = tid & 63;
-        const int r = lane & 15, g = lane >> 4;  // column (query head), group of 16 lanes
-        const Keys keys = visible_keys(a, c, b);
-        const int rt = unit % row_tiles, hk = unit / row_tiles;
-        const int head0 = hk * G + rt * kRows;
-        const int n_rows = min(G - rt * kRows, kRows);
+    const int rt = unit % row_tiles, hk = unit / row_tiles;
+    const int head0 = hk * G + rt * kRows, n_rows = min(G - rt * kRows, kRows);
+    const DecodeUnit u = {a, visible_keys(a, c, b), c.table + b * c.ld_table, b, hk, head0, n_rows, D};
+    const bool wide = wide_rows(a);
+    const int tid = threadIdx.x, lane = tid & 63, wid = uniform(tid >> 6);
+    const int r = lane & 15, g = lane >> 4;
+    floatx4_t o[DP / 16];
+    float M, l;
+    narrow_wave<DP, PAGE16, kWaves>(a, c, u, t0 + wid, t1, sv[wid], o, &M, &l);
 
-        bf16x8_t qf[KS];
-        {
-            const uint16_t *src =
-                a.q + b * a.ldq + static_cast<int64_t>(head0 + min(r, n_rows - 1)) * D;
+    // Join the waves.
+    constexpr int kRow = kNarrowRow<DP>;
+    if (g == 0) {
+        sm[wid][r] = M;
+        sl[wid][r] = l;
+    }
+    float *my_o = reinterpret_cast<float *>(sv[wid]);
 #pragma unroll
-            for (int s = 0; s < KS; ++s) {
-                const int d = 32 * s + 8 * g;
-                const uintx4_t v = *reinterpret_cast<const uintx4_t *>(src + min(d, D - 8));
-                qf[s] = __builtin_bit_cast(bf16x8_t, d < D ? v : uintx4_t{0, 0, 0, 0});
-            }
+    for (int d = 0; d < DP / 16; ++d)
+        *reinterpret_cast<floatx4_t *>(&my_o[r * kRow + 16 * d + 4 * g]) = o[d];
+    __syncthreads();
+    const Partial part = partial(a.work, plan, blockIdx.x, min(G, kRows), D);
+    for (int e = tid; e < n_rows * (DP / 4); e += kWaves * 64) {
+        const int row = e / (DP / 4), d = e % (DP / 4) * 4;
+        if (d >= D) continue;
+        float m = sm[0][row], sum = 0.0f;
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w][row]);
+        floatx4_t v = floatx4_t(0.0f);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const float f = __builtin_amdgcn_exp2f(sm[w][row] - m);
+            sum += f * sl[w][row];
+            v += f * *reinterpret_cast<const floatx4_t *>(reinterpret_cast<const float *>(sv[w]) +
+                                                          row * kRow + d);
         }
-
-        const int32_t *table = c.table + b * c.ld_table;
-        const int64_t head_off = static_cast<int64_t>(hk) * c.head_stride;
-        const auto visible = [&](int p) {
-            return (p <= keys.last) & ((p >= keys.lo) | (p < a.sinks));
-        };
-        // 16 keys as they are read: the page offset of a visible key among them (of the newest key
-        // if there is none), and that key. Keys that are not visible are read from it: finite
-        // values, whose weight is 0.
-        struct Span {
-            int start, safe;
-            int64_t page;
-        };
-        const auto safe_key = [&](int s0) {
-            if (s0 < a.sinks && s0 < keys.lo) return s0;
-            return s0 > keys.last || s0 + 15 < keys.lo ? keys.last : max(s0, keys.lo);
-        };
-        const auto page_offset = [&](int page) {
-            page = page < 0 ? 0 : (page >= c.n_pages ? c.n_pages - 1 : page);
-            return static_cast<int64_t>(page) * c.page_stride + head_off;
-        };
-        // Eight elements from element `col` on of row i (0..15) of a span. (The page's address is
-        // uniform where the span lies in one page: a scalar base and a 32-bit offset in bytes.)
-        const auto load_row = [&](const uint16_t *kv, const Span &sp, int i, int col) {
-            const int p = sp.start + i;
-            const int from = visible(p) ? p : sp.safe;
-            const int64_t page =
-                PAGE16 ? sp.page : page_offset(read_const(table + (from >> c.page_shift)));
-            const uint32_t off = (from & c.page_mask) * c.slot_stride + col;
-            return *reinterpret_cast<const uintx4_t *>(
-                reinterpret_cast<const char *>(kv + page) + 2u * off);
-        };
-
-        // The next tile to be fetched, and the one after it: their spans' keys, and the table
-        // entries on their way.
-        Span next[2];
-        int entry[2] = {0, 0};
-        const auto look_up = [&](int t) {
-            if (!PAGE16) return;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-                entry[u] = read_const(table + (safe_key(keys.start(t) + 16 * u) >> c.page_shift));
-        };
-        const auto locate = [&](int t) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                next[u].start = keys.start(t) + 16 * u;
-                next[u].safe = safe_key(next[u].start);
-                next[u].page = page_offset(entry[u]);
-            }
-        };
-        // Dims past D repeat the row's last chunk: they meet zeros of q, or outputs that are not
-        // kept.
-        const int v_row = lane / kChunks, v_chunk = min(8 * (lane % kChunks), D - 8);
-        uintx4_t rk[2][KS], rv[kVLoads];
-        const auto fetch_k = [&] {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int s = 0; s < KS; ++s)
-                    rk[u][s] = load_row(c.k, next[u], r, min(32 * s + 8 * g, D - 8));
-        };
-        const auto fetch_v = [&] {
-#pragma unroll
-            for (int i = 0; i < kVLoads; ++i)
-                rv[i] = load_row(c.v, next[i * kVRows / 16], i * kVRows % 16 + v_row, v_chunk);
-        };
-
-        floatx4_t o[DT];
-#pragma unroll
-        for (int i = 0; i < DT; ++i) o[i] = floatx4_t(0.0f);
-        float M = kNoMax, l = 0.0f;
-
-        // One tile; with MORE, the wave's next tile is fetched on the way, and the one after that
-        // looked up; with ANY, values may be infinite or NaN.
-        const auto step = [&](auto more, auto any, int t) {
-            constexpr bool MORE = decltype(more)::value, ANY = decltype(any)::value;
-            const int k0 = keys.start(t), after = min(t + 2 * kWaves, t1 - 1);
-            if constexpr (MORE) look_up(after);
-            floatx4_t s[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                s[u] = floatx4_t(0.0f);
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8_t, rk[u][ks]), qf[ks], s[u], 0, 0, 0);
-            }
-            phase_fence();
-            if constexpr (MORE) fetch_k();
-            phase_fence();
-#pragma unroll
-            for (int i = 0; i < kVLoads; ++i) {
-                uintx4_t kind, *to = reinterpret_cast<uintx4_t *>(
-                                   &my_v[(i * kVRows + v_row) * kRow + 8 * (lane % kChunks)]);
-                *to = ANY ? split_values<kMinus, kNan>(rv[i], &kind) : rv[i];
-            }
-            phase_fence();
-            __builtin_amdgcn_wave_barrier();
-            if constexpr (MORE) {
-                fetch_v();
-                locate(after);
-            }
-            phase_fence();
-
-            float mx = -INFINITY;
-            bool ok[2][4];
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    ok[u][i] = visible(k0 + 16 * u + 4 * g + i);
-                    s[u][i] = s[u][i] * cs;
-                    mx = ok[u][i] ? fmaxf(mx, s[u][i]) : mx;
-                }
-            mx = fmaxf(mx, __shfl_xor(mx, 16, kWave));
-            mx = fmaxf(mx, __shfl_xor(mx, 32, kWave));
-            if (__any(mx > M + kSlack)) {
-                const float M2 = fmaxf(M, mx);
-                const float f = __builtin_amdgcn_exp2f(M - M2);
-                M = M2;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < DT; ++d) o[d] *= f;
-            }
-            uintx4_t hi, lo;
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; i += 2) {
-                    const float p0 = ok[u][i] ? __builtin_amdgcn_exp2f(s[u][i] - M) : 0.0f;
-                    const float p1 = ok[u][i + 1] ? __builtin_amdgcn_exp2f(s[u][i + 1] - M) : 0.0f;
-                    l += p0 + p1;
-                    const uint32_t w = pack_bf16(p0, p1);
-                    hi[2 * u + i / 2] = w;
-                    lo[2 * u + i / 2] = pack_bf16(p0 - __uint_as_float(w << 16),
-                                                  p1 - __uint_as_float(w & 0xFFFF0000u));
-                }
-            // slots 8 g + 0..3 are keys 4 g + 0..3, slots 8 g + 4..7 keys 16 + 4 g + 0..3
-            const uint16_t *vp = &my_v[(4 * g + r / 4) * kRow + 4 * (r & 3)];
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                const uintx2_t v0 = lds_read_transposed(vp + 16 * d);
-                const uintx2_t v1 = lds_read_transposed(vp + 16 * kRow + 16 * d);
-                const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
-                const bf16x8_t vf = __builtin_bit_cast(bf16x8_t, vv);
-                o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8_t, hi),
-                                                               o[d], 0, 0, 0);
-                o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, __builtin_bit_cast(bf16x8_t, lo),
-                                                               o[d], 0, 0, 0);
-            }
-            asm volatile("" ::: "memory");
-            __builtin_amdgcn_wave_barrier();
-            if constexpr (ANY) {
-                // the values that are not finite, counted by kind for the keys that are seen
-                uintx4_t seen;  // bf16 ones where weights are
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2)
-                        seen[2 * u + i / 2] =
-                            (ok[u][i] && s[u][i] != -INFINITY ? 0x3F80u : 0) |
-                            (ok[u][i + 1] && s[u][i + 1] != -INFINITY ? 0x3F800000u : 0);
-#pragma unroll
-                for (int i = 0; i < kVLoads; ++i) {
-                    uintx4_t kind;
-                    split_values<kMinus, kNan>(rv[i], &kind);
-                    *reinterpret_cast<uintx4_t *>(
-                        &my_v[(i * kVRows + v_row) * kRow + 8 * (lane % kChunks)]) = kind;
-                }
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_wave_barrier();
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const uintx2_t v0 = lds_read_transposed(vp + 16 * d);
-                    const uintx2_t v1 = lds_read_transposed(vp + 16 * kRow + 16 * d);
-                    const uintx4_t vv = {v0[0], v0[1], v1[0], v1[1]};
-                    const floatx4_t n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                        __builtin_bit_cast(bf16x8_t, vv), __builtin_bit_cast(bf16x8_t, seen),
-                        floatx4_t(0.0f), 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        o[d][i] = add_kinds<64, 4096>(o[d][i], static_cast<int>(n[i]));
-                }
-                asm volatile("" ::: "memory");
-                __builtin_amdgcn_wave_barrier();
-            }
-        };
-        int t = t0 + wid;
-        if (t < t1) {
-            look_up(t);
-            locate(t);
-            fetch_k();
-            fetch_v();
-            look_up(min(t + kWaves, t1 - 1));
-            locate(min(t + kWaves, t1 - 1));
-            if (t + kWaves < t1) {
-                do {
-                    step(std::true_type{}, std::false_type{}, t);
-                    t += kWaves;
-                } while (t + kWaves < t1);
-            }
-            step(std::false_type{}, std::false_type{}, t);
-        }
-        // An infinite value times the lower part of its weight, or a weight of 0 (where the row
-        // that stands in for a hidden one holds it), is not that infinity. So a wave whose sums are
-        // not finite goes through its tiles again, its values split into finite ones and others.
-        float odd[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) odd[i] = fmaf(o[d][i], 0.0f, odd[i]);
-        if (__builtin_expect(__any(odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f), 0)) {
-            M = kNoMax;
-            l = 0.0f;
-#pragma unroll
-            for (int d = 0; d < DT; ++d) o[d] = floatx4_t(0.0f);
-            for (t = t0 + wid; t < t1; t += kWaves) {
-                look_up(t);
-                locate(t);
-                fetch_k();
-                fetch_v();
-                step(std::false_type{}, std::true_type{}, t);
-            }
-        }
-
-        // Join the waves: lane (g, r) holds dims 16 d + 4 g + 0..3 of head r.
-        l += __shfl_xor(l, 16, kWave);
-        l += __shfl_xor(l, 32, kWave);
-        if (g == 0) {
-            sm[wid][r] = M;
-            sl[wid][r] = l;
-        }
-        float *my_o = reinterpret_cast<float *>(my_v);
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-            *reinterpret_cast<floatx4_t *>(&my_o[r * kRow + 16 * d + 4 * g]) = o[d];
-        __syncthreads();
-        const bool wide = wide_rows(a);
-        const int slot_rows = min(G, kRows);
-        const Partial part = partial(a.work, plan, blockIdx.x, slot_rows, D);
-        for (int e = tid; e < n_rows * (DP / 4); e += kWaves * 64) {
-            const int row = e / (DP / 4), d = e % (DP / 4) * 4;
-            if (d >= D) continue;
-            float m = sm[0][row], sum = 0.0f;
-#pragma unroll
-            for (int w = 1; w < kWaves; ++w) m = fmaxf(m, sm[w][row]);
-            floatx4_t v = floatx4_t(0.0f);
-#pragma unroll
-            for (int w = 0; w < kWaves; ++w) {
-                const float f = __builtin_amdgcn_exp2f(sm[w][row] - m);
-                sum += f * sl[w][row];
-                v += f * *reinterpret_cast<const floatx4_t *>(
-                             reinterpret_cast<const float *>(sv[w]) + row * kRow + d);
-            }
-            if (whole) {
-                v *= inverse_sum(sum);
-                store_out4(a.y, b * a.ldy + static_cast<int64_t>(head0 + row) * D + d, v, a.out_f32,
-                           wide);
-                if (a.lse && d == 0)
-                    a.lse[static_cast<int64_t>(b) * a.n_heads + head0 + row] = log_sum(m, sum);
-            } else {
-                *reinterpret_cast<floatx4_t *>(part.o + row * D + d) = v;
-                if (d == 0) {
-                    part.m[row] = m;
-                    part.l[row] = sum;
-                }
+        if (whole) {
+            v *= inverse_sum(sum);
+            store_out4(a.y, b * a.ldy + static_cast<int64_t>(head0 + row) * D + d, v, a.out_f32,
+                       wide);
+            if (a.lse && d == 0)
+                a.lse[static_cast<int64_t>(b) * a.n_heads + head0 + row] = log_sum(m, sum);
+        } else {
+            *reinterpret_cast<floatx4_t *>(part.o + row * D + d) = v;
+            if (d == 0) {
+                part.m[row] = m;
+                part.l[row] = sum;
             }
         }
     }

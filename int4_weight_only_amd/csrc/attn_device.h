@@ -20,6 +20,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Running maximum before the first key: the lowest finite number, so that no score lies below it and
 // no infinity is subtracted from another.
 constexpr float kNoMax = -3.40282347e38f;
+// log2 of how far a weight may pass 1 before the sums are rescaled.
+constexpr int kScoreSlack = 8;
 
 // Four bf16 rows of 16 columns, transposed on the way out of LDS: in each group of 16 lanes, lane i
 // addresses the 8 bytes at columns 4 (i % 4) of row i / 4 and receives column i of the four rows.
@@ -90,6 +92,12 @@ __device__ __forceinline__ bool wide_rows(const AttnArgs &a) {
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
 __device__ __forceinline__ float log_sum(float m, float l) {
     return l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
+}
+
+// The same value, as if unknown: nothing computed from it is taken for what was computed before.
+__device__ __forceinline__ int unknown(int v) {
+    asm volatile("" : "+v"(v));
+    return v;
 }
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }

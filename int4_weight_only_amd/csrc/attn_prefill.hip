@@ -108,16 +108,18 @@ struct PrefillRows {
         KvView c;
         int splits;
     };
+    struct State {};
     static constexpr bool kTwoTables = false;
 
     template <int DP, int KT>
-    __device__ __forceinline__ static bool find(const Args &args, int wid, int lane, uint16_t *,
-                                                uint16_t *, int *, TileRows *r) {
+    __device__ __forceinline__ static bool find(const Args &args, const State &, int wid, int lane,
+                                                uint16_t *, uint16_t *, TileRows *r) {
         const AttnArgs &a = args.a;
         const KvView &c = args.c;
         const int G = a.n_heads / c.n_kv;
         r->hk = blockIdx.x % c.n_kv;
         r->part = blockIdx.x / c.n_kv % args.splits;
+        r->part_end = r->part + 1;
         r->parts = args.splits;
         Tile t;
         if (!find_tile<kTileRows>(c, a.q_start, a.T, G, blockIdx.x / c.n_kv / args.splits, &t))
@@ -129,8 +131,8 @@ struct PrefillRows {
         r->head = r->hk * G + (safe_row - tok * G);
         r->live = row < t.rows;
         const auto position = [&](int row) {
-            const int at = min(row, t.rows - 1) / G;
-            return CROSS ? t.pos0 + t.rows / G - 1 : t.pos0 + at;
+            const int last = t.rows - 1;
+            return t.pos0 + (CROSS ? last : min(row, last)) / G;
         };
         r->pos = position(row);
         r->tile_first = position(t.row0);
@@ -143,19 +145,19 @@ struct PrefillRows {
     __device__ __forceinline__ static bool is_partial(const Args &args, const TileRows &) {
         return args.splits > 1;
     }
-    __device__ __forceinline__ static void write_sums(const Args &args, const TileRows &r, float m,
-                                                      float l) {
-        const AttnArgs &a = args.a;
-        const Partials p = partials(a.work, a.T * a.n_heads, args.splits, r.part, args.c.head_dim);
-        const int64_t pair = r.token * static_cast<int64_t>(a.n_heads) + r.head;
-        p.ml[2 * pair] = m;
-        p.ml[2 * pair + 1] = l;
-    }
-    __device__ __forceinline__ static float *sums(const Args &args, const TileRows &r) {
+    // The lane's row of partial sums; its maximum and sum of weights are written where `lead`.
+    __device__ __forceinline__ static float *write_sums(const Args &args, const State &,
+                                                        const TileRows &r, float m, float l,
+                                                        bool lead) {
         const AttnArgs &a = args.a;
         const int D = args.c.head_dim;
-        return partials(a.work, a.T * a.n_heads, args.splits, r.part, D).o +
-               (r.token * static_cast<int64_t>(a.n_heads) + r.head) * D;
+        const Partials p = partials(a.work, a.T * a.n_heads, args.splits, r.part, D);
+        const int64_t pair = r.token * static_cast<int64_t>(a.n_heads) + r.head;
+        if (lead) {
+            p.ml[2 * pair] = m;
+            p.ml[2 * pair + 1] = l;
+        }
+        return p.o + pair * D;
     }
 };
 
@@ -258,20 +260,8 @@ size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &c, int wind
 hipError_t launch_attn_prefill(const AttnArgs &a, const KvView &c, hipStream_t stream) {
     return launch<false>(a, c, stream);
 }
-
-// Cross attention: the decode kernel where each sequence has one row.
-bool attn_cross_supported(int64_t T, int n_heads, const KvView &c, bool single) {
-    return single ? attn_decode_supported(n_heads, c, 0, 0)
-                  : attn_prefill_supported(T, n_heads, c, 0, 0);
-}
-
-size_t attn_cross_work_bytes(int64_t T, int n_heads, const KvView &c, bool single) {
-    return single ? attn_decode_work_bytes(n_heads, c, 0, 0)
-                  : attn_prefill_work_bytes(T, n_heads, c, 0, 0);
-}
-
-hipError_t launch_attn_cross(const AttnArgs &a, const KvView &c, hipStream_t stream) {
-    return a.q_start ? launch<true>(a, c, stream) : launch_attn_decode(a, c, stream);
+hipError_t launch_attn_prefill_cross(const AttnArgs &a, const KvView &c, hipStream_t stream) {
+    return launch<true>(a, c, stream);
 }
 
 }  // namespace w4

@@ -20,19 +20,20 @@
 // that one can multiply while the other turns scores into weights.
 #pragma once
 
+#include <type_traits>
+
 #include "attn_device.h"
 
 namespace w4 {
 
 constexpr int kTileWaves = 4, kTileRows = 32 * kTileWaves;
-constexpr int kSlack = 8;
 constexpr float kFar = 1 << 20;
 
 // What a workgroup computes. Rows::find fills it; every wave of the workgroup finds the same but for
 // what belongs to a lane's row and a wave's rows.
 struct TileRows {
     int hk;           // key-value head
-    int part, parts;  // the share of the key tiles
+    int part, part_end, parts;  // the share of the key tiles: from part to part_end of `parts`
     // of the lane's row, or of a row that exists where there is none: token row, query head, position
     int token, head, pos;
     bool live;
@@ -44,9 +45,10 @@ struct TileRows {
     const int32_t *first_table;
     int cut;
     bool from_cut, to_cut;
-    // (of Rows with two tables: rows of a prefix, rows written as they are, place of partial sums)
-    bool of_prefix, direct;
-    int extra;
+    // (of Rows that cut units into pieces: rows of a prefix; rows written as they are; the first of the
+    // unit's pieces, how many there are, and where the piece after this one begins)
+    bool of_prefix, direct, first_piece;
+    int pieces, next;
 };
 
 // The key tiles that the rows of a workgroup see: those of the sinks, then those from `lo` on. Where
@@ -75,6 +77,11 @@ struct KeyTiles {
             lo_tile = max(lo / KT, n_sink);
             n = last < 0 ? 0 : n_sink + last / KT + 1 - lo_tile;
         }
+    }
+    // Where share `part` of `parts` begins. (As many shares as tiles: a plan's own numbers.)
+    __device__ __forceinline__ int share(int part, int parts) const {
+        if (TABLES && parts == n) return part;
+        return static_cast<int>(static_cast<int64_t>(n) * part / parts);
     }
     __device__ __forceinline__ int number(int p, int cut) const {
         return p / KT + (p < cut ? 0 : twice);
@@ -118,12 +125,6 @@ __device__ __forceinline__ void tile_barrier() {
     __builtin_amdgcn_s_waitcnt(wait_vm<0>() & 0xF0FF);  // vmcnt(0) and lgkmcnt(0)
     __builtin_amdgcn_s_barrier();
     phase_fence();
-}
-
-// The same value, as if unknown: nothing computed from it is taken for what was computed before.
-__device__ __forceinline__ int unknown(int v) {
-    asm volatile("" : "+v"(v));
-    return v;
 }
 
 // A tile in LDS: direct loads from memory, which lay 64 lanes of 16 bytes down in a row, put kSpan
@@ -195,9 +196,11 @@ __device__ __forceinline__ Args args_again() {
 // unknown: whatever the two passes shared would occupy registers throughout, and the first pass'
 // loop lost its order of reads or spilled (one prompt of 2048 tokens: 54 us for 49; 2 chunks of up
 // to 4096, 256 dims, window 1024: 201 us for 176).
+// Returns what find left in `next`.
 template <class Rows, int DP, int KT, int PAGES, bool ANY>
-__device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint16_t *sk0,
-                                          uint16_t *sk1, uint16_t *sv0, uint16_t *sv1, int *votes) {
+__device__ __forceinline__ int attn_tile(const typename Rows::Args &args,
+                                          const typename Rows::State &state, uint16_t *sk0,
+                                         uint16_t *sk1, uint16_t *sv0, uint16_t *sv1, int *votes) {
     constexpr bool TABLES = Rows::kTwoTables;
     const AttnArgs &a = args.a;
     const KvView &c = args.c;
@@ -208,13 +211,15 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
     static_assert(kLoads * NW * kSpan == KT, "every wave stages the same number of rows");
     using L = TileLayout<DP>;
     constexpr int DT = DP / 32, KS = DP / 16, SUB = KT / 32;
-    const int tid = ANY ? unknown(threadIdx.x) : threadIdx.x;
+    // (TABLES: called in a loop over units, out of which nothing that takes registers is to move)
+    const int tid = ANY || TABLES ? unknown(threadIdx.x) : threadIdx.x;
     const int lane = tid & 63;
     const int wid = uniform(tid >> 6);
     const int D = c.head_dim;
     const int half = lane >> 5;
     TileRows t;
-    if (!Rows::template find<DP, KT>(args, wid, lane, sk0, sv0, votes, &t)) return;
+    t.next = 0;
+    if (!Rows::template find<DP, KT>(args, state, wid, lane, sk0, sv0, &t)) return t.next;
     const int hk = t.hk, pos = t.pos, tile_last = t.tile_last;
 
     // Key tiles: those of the sinks, then those from the oldest key in a row's window on; of them
@@ -222,9 +227,8 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
     const int lo = a.window > 0 ? max(t.tile_first - a.window + 1, 0) : 0;
     const int sinks_end = a.window > 0 ? a.sinks : 0;
     const KeyTiles<KT, TABLES> tiles(t, lo, sinks_end);
-    const int it0 = static_cast<int>(static_cast<int64_t>(tiles.n) * t.part / t.parts);
-    const int n_iter =
-        static_cast<int>(static_cast<int64_t>(tiles.n) * (t.part + 1) / t.parts) - it0;
+    const int it0 = tiles.share(t.part, t.parts);
+    const int n_iter = tiles.share(t.part_end, t.parts) - it0;
     const auto tile_key = [&](int it) { return tiles.key(it + it0); };
     // With two tables: where the keys of a tile end that its table holds, and where they begin.
     const auto tile_end = [&](int it) {
@@ -492,7 +496,7 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
             for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[u][i]);
         mx = max_of_halves(mx) * cs;
         float f = 1.0f;
-        *rose = __any(mx > M + kSlack);
+        *rose = __any(mx > M + kScoreSlack);
         if (*rose) {
             const float M2 = fmaxf(M, mx);
             f = __builtin_amdgcn_exp2f(M - M2);
@@ -560,33 +564,45 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
         for (int w = 0; w < NW; ++w) any |= votes[w] != 0;
         return any;
     };
-    // What is written of a row: its maximum and sum of weights (or its lse), and 32 of its dims.
-    const auto write_row = [&]() __attribute__((always_inline)) {
+    // What is written of a row: its maximum and sum of weights (or its lse) where `lead`, and N times
+    // 32 of its dims, from 32 d0 on.
+    const auto write = [&](bool lead, int d0, auto n, const floatx16_t *o)
+                           __attribute__((always_inline)) {
+        constexpr int N = decltype(n)::value;
         l += other_half(l);
-        if (!t.live || half != 0) return;
-        if constexpr (TABLES) Rows::write_record(args, t);
-        if (Rows::is_partial(args, t))
-            Rows::write_sums(args, t, M, l);
-        else if (a.lse)
-            a.lse[t.token * static_cast<int64_t>(a.n_heads) + t.head] = log_sum(M, l);
-    };
-    const auto write_dims = [&](int d, const floatx16_t &o) __attribute__((always_inline)) {
-        // (shares without keys: their sum is 0, the weighted sums are not read)
-        const bool part = Rows::is_partial(args, t);
-        if (!t.live || (part && n_iter == 0)) return;
-        const int64_t base = t.token * a.ldy + static_cast<int64_t>(t.head) * D;
+        if (!t.live) return;
+        lead &= half == 0;
+        if (Rows::is_partial(args, t)) {
+            // (shares without keys: their sum is 0, the weighted sums are not read)
+            float *to = Rows::write_sums(args, state, t, M, l, lead) + 4 * half;
+            if (n_iter == 0) return;
+#pragma unroll
+            for (int d = 0; d < N; ++d)
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int col = 32 * (d0 + d) + 8 * g;  // (D is a multiple of 8)
+                    if (col < D)
+                        *reinterpret_cast<floatx4_t *>(to + col) = floatx4_t{
+                            o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
+                }
+            return;
+        }
+        if constexpr (TABLES) {
+            if (lead) Rows::write_record(args, state, t);
+        }
+        if (lead && a.lse) a.lse[t.token * static_cast<int64_t>(a.n_heads) + t.head] = log_sum(M, l);
+        const int64_t base = t.token * a.ldy + static_cast<int64_t>(t.head) * D + 4 * half;
         const float inv = inverse_sum(l);
         const bool wide = wide_rows(a);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const int col = 32 * d + 8 * g + 4 * half;
-            if (col >= D) continue;
-            floatx4_t v = {o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]};
-            if (part)
-                *reinterpret_cast<floatx4_t *>(Rows::sums(args, t) + col) = v;
-            else
+        for (int d = 0; d < N; ++d)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int col = 32 * (d0 + d) + 8 * g;
+                if (col >= D) continue;
+                const floatx4_t v = {o[d][4 * g], o[d][4 * g + 1], o[d][4 * g + 2], o[d][4 * g + 3]};
                 store_out4(a.y, base + col, v * inv, a.out_f32, wide);
-        }
+            }
     };
 
     if constexpr (ANY) {
@@ -612,14 +628,9 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
                 weigh_any(sv0, d0);
                 tile_barrier();
             }
-            if (d0 == 0)
-                write_row();
-            else
-                l += other_half(l);
-#pragma unroll
-            for (int d = 0; d < kAnyDims; ++d) write_dims(d0 + d, o[d]);
+            write(d0 == 0, d0, std::integral_constant<int, kAnyDims>{}, o);
         }
-        return;
+        return t.next;
     }
     if (n_iter > 0) {
         look_up(0);
@@ -659,16 +670,14 @@ __device__ __forceinline__ void attn_tile(const typename Rows::Args &args, uint1
             for (int i = 0; i < 16; ++i) odd[i % 4] = fmaf(o[d][i], 0.0f, odd[i % 4]);
         const bool again = odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f || is_far();
         if (__builtin_expect(block_any(again), 0)) {
-            if constexpr (TABLES) __syncthreads();  // (the votes are read no more)
-            attn_tile<Rows, DP, KT, PAGES, true>(args_again<typename Rows::Args>(), sk0, sk0, sv0,
-                                                 sv0, votes);
-            return;
+            attn_tile<Rows, DP, KT, PAGES, true>(args_again<typename Rows::Args>(), state, sk0, sk0,
+                                                 sv0, sv0, votes);
+            return t.next;
         }
     }
 
-    write_row();
-#pragma unroll
-    for (int d = 0; d < DT; ++d) write_dims(d, o[d]);
+    write(true, 0, std::integral_constant<int, DT>{}, o);
+    return t.next;
 }
 
 template <class Rows, int DP, int KT, int PAGES>
@@ -682,7 +691,7 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_tile_kernel(typename Rows::Args 
     __shared__ __attribute__((aligned(16))) uint16_t sv0[KT / L::kSpan * L::kValueBlock];
     __shared__ __attribute__((aligned(16))) uint16_t sv1[KT / L::kSpan * L::kValueBlock];
     __shared__ int votes[kTileWaves];
-    attn_tile<Rows, DP, KT, PAGES, false>(args, sk0, sk1, sv0, sv1, votes);
+    attn_tile<Rows, DP, KT, PAGES, false>(args, {}, sk0, sk1, sv0, sv1, votes);
 }
 
 // Keys of a tile, by head size.

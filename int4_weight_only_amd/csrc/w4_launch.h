@@ -163,13 +163,13 @@ size_t attn_decode_work_bytes(int n_heads, const KvView &cache, int window, int 
 hipError_t launch_attn_decode(const AttnArgs &a, const KvView &cache, hipStream_t stream);
 size_t attn_prefill_work_bytes(int64_t T, int n_heads, const KvView &cache, int window, int sinks);
 hipError_t launch_attn_prefill(const AttnArgs &a, const KvView &cache, hipStream_t stream);
+// The same with every key of its sequence seen by each row.
+hipError_t launch_attn_prefill_cross(const AttnArgs &a, const KvView &cache, hipStream_t stream);
 
-// Attention of sequences that share prefixes, and cross attention (attn_shared.hip, attn_prefill.hip).
-// Without q_start a.T is the number of sequences.
-bool attn_shared_supported(int64_t T, int n_heads, const KvView &cache, const Prefixes &prefixes,
-                           int window, int sinks);
-size_t attn_shared_work_bytes(int64_t T, int n_heads, const KvView &cache,
-                              const Prefixes &prefixes, int window, int sinks);
+// Attention of sequences that share prefixes, and cross attention (attn_units.hip). Without q_start
+// a.T is the number of sequences.
+size_t attn_shared_work_bytes(int64_t T, int n_heads, const KvView &cache);
+bool attn_shared_supported(int64_t T, int n_heads, const KvView &cache, const Prefixes &prefixes);
 hipError_t launch_attn_shared(const AttnArgs &a, const KvView &cache, const Prefixes &prefixes,
                               hipStream_t stream);
 // (single: without q_start)

@@ -47,7 +47,7 @@ def test_a_bad_cache_is_refused(kw, status):
 @pytest.mark.parametrize("kw,status", [
     (dict(prefix_of=None), NULL), (dict(table=None), NULL), (dict(len=None), NULL),
     (dict(n_prefixes=0), SHAPE), (dict(table_cols=0), SHAPE), (dict(ld_table=4), SHAPE),
-    (dict(n_prefixes=2049), RANGE), (dict(table_cols=1 << 25, ld_table=1 << 25), RANGE),
+    (dict(n_prefixes=257), RANGE), (dict(table_cols=1 << 25, ld_table=1 << 25), RANGE),
     (dict(ld_table=1 << 31), RANGE), (dict(prefix_of=X + 2), ALIGN), (dict(table=Y + 1), ALIGN),
     (dict(len=Z + 3), ALIGN)])
 def test_bad_prefixes_are_refused(kw, status):

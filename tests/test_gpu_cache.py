@@ -192,7 +192,7 @@ def test_shared_long_and_split():
     share(rng, [6000], [0] * 4, [8000, 6001, 9000, 6400], None, 4, 2, 256, 128, 4500, 70)
 
 
-@pytest.mark.parametrize("B,prefixes", [(65, 3), (300, 70), (1500, 1), (1100, 1100)])
+@pytest.mark.parametrize("B,prefixes", [(65, 3), (300, 70), (1500, 1), (1100, 256)])
 def test_shared_many_sequences(B, prefixes):
     rng = np.random.default_rng([9, B, prefixes])
     plen = rng.integers(0, 80, prefixes)
