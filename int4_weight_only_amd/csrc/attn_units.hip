@@ -187,7 +187,8 @@ struct Units {
     // Length of each on the line; of all of them.
     __device__ __forceinline__ static int length(const Place &at, int rows, int tiles) {
         const int cost = unit_cost(rows, tiles);
-        return at.whole ? divide(cost + at.span - 1, at.span) * at.span : cost;
+        // (no piece without a tile but the first)
+        return at.whole ? min(divide(cost + at.span - 1, at.span), max(tiles, 1)) * at.span : cost;
     }
     __device__ __forceinline__ int lengths(const Place &at, bool narrow, int rows, int tiles) const {
         return is_narrow(rows) == narrow ? units_of(rows) * length(at, rows, tiles) : 0;
