@@ -1,6 +1,6 @@
 """A decoder of int4 linears end to end: the layer operators as a serving program calls them.
 
-    python -m examples.decoder [--layers 4] [--prompts 700,2000,33] [--steps 32]
+    python -m examples.decoder [--layers 4] [--prompts 700,2000,33] [--steps 32] [--system 0]
 
 A batch of prompts goes through the layers in one pass (w4_attn_prefill), then every sequence gets one
 token a step (w4_attn_decode), the step recorded once as a HIP graph and replayed. Weights are random
@@ -13,6 +13,10 @@ One layer, with the residual stream h in fp32:
     a    = attention over the cache                      w4_attn_prefill / w4_attn_decode
     y, h = residual_norm(a Wo^T, h)                      w4_residual_norm
     out  = (silu(y Wgate^T) * y Wup^T) Wdown^T           w4_gemv_glu, w4_gemv / w4_gemm
+
+With --system N the prompts follow one system prompt of N tokens. Its keys and values are made once and
+shared: the tables of every pass, the recorded step's too, are made on the GPU from the pool's free
+pages (w4_batch_tables), and attention reads the shared keys once for all sequences (w4_attn_shared).
 """
 import argparse
 from dataclasses import dataclass
@@ -61,6 +65,49 @@ class Cache:
         return self.k[i], self.v[i], self.table, self.kv_len
 
 
+class SharedCache:
+    """A pool of `pages` pages for `n` sequences that may share the system prompt, whose keys are those
+    of one sequence more, the last. Which pages a sequence has is known on the GPU alone."""
+
+    def __init__(self, shape, n, pages, most, device):
+        def ints(*size):
+            return torch.zeros(size, dtype=torch.int32, device=device)
+
+        self.shape, self.n = shape, n
+        self.table = ints(n + 1, -(-most // shape.page_size))
+        self.kv_len, self.spans = ints(n + 1), ints(n + 1, 2)
+        self.ring = torch.arange(pages, dtype=torch.int32, device=device)
+        self.state = ints(3)
+        self.state[1] = pages
+        self.prefix_of = torch.full((n + 1,), -1, dtype=torch.int32, device=device)
+        self.prefix_len = ints(1)
+        size = (shape.layers, pages, shape.page_size, shape.kv_heads, shape.head_dim)
+        self.k = torch.empty(size, dtype=torch.bfloat16, device=device)
+        self.v = torch.empty(size, dtype=torch.bfloat16, device=device)
+
+    def layer(self, i):
+        return self.k[i], self.v[i], self.table, self.kv_len
+
+    def advance(self, n_new, T):
+        """Pages for n_new[b] tokens of each sequence, T in all (-1: the sequence ends and its pages
+        are free again); returns where each sequence's rows begin."""
+        return w4.w4_batch_tables(self.kv_len, n_new, self.spans, self.table, self.shape.page_size,
+                                  self.ring, self.state, T, in_place=True)[0]
+
+    def share(self, b):
+        """Sequence b begins after the system prompt."""
+        P = self.kv_len[self.n]
+        self.prefix_len[0] = P
+        self.prefix_of[b] = 0
+        self.kv_len[b] = P
+        self.spans[b] = P // self.shape.page_size  # (a page that it shares in part is not its own)
+
+    def attention(self, i, q, q_start):
+        s = self.shape
+        return w4.w4_attn_shared(q, *self.layer(i), self.prefix_of, self.table[self.n:],
+                                 self.prefix_len, q_start=q_start, window=s.window, sinks=s.sinks)
+
+
 class Decoder:
     def __init__(self, shape, device="cuda", seed=0):
         self.shape = s = shape
@@ -99,7 +146,9 @@ class Decoder:
                                        residual_out=None if out is None else h)
             qkv = w4.w4_linear(y, *layer["qkv"])
             q = w4.w4_rope_append(qkv, s.heads, *cache.layer(i), self.inv_freq, q_start)
-            if q_start is None:
+            if isinstance(cache, SharedCache):
+                a = cache.attention(i, q, q_start)
+            elif q_start is None:
                 a = w4.w4_attn_decode(q, *cache.layer(i), window=s.window, sinks=s.sinks)
             else:
                 a = w4.w4_attn_prefill(q, *cache.layer(i), q_start, window=s.window,
@@ -120,6 +169,11 @@ class Decoder:
         cache.kv_len += ends[1:] - ends[:-1]
         return self.forward(x.float().clone(), cache, ends)
 
+    def shared_pass(self, x, n_new, cache):
+        """A pass over n_new[b] tokens (int32 [n + 1], on the GPU) of each sequence of a SharedCache, x
+        [sum of n_new][hidden] one after the other."""
+        return self.forward(x.float().clone(), cache, cache.advance(n_new, x.shape[0]))
+
     def step(self, x, cache):
         """One token of each sequence, x [n_seqs][hidden]."""
         cache.kv_len += 1
@@ -132,6 +186,7 @@ def main(argv=None):
     p.add_argument("--prompts", default="700,2000,33", help="tokens of each prompt")
     p.add_argument("--steps", type=int, default=32, help="tokens generated per sequence")
     p.add_argument("--window", type=int, default=0, help="attention window (0: none)")
+    p.add_argument("--system", type=int, default=0, help="tokens of a shared system prompt")
     args = p.parse_args(argv)
     lens = [int(n) for n in args.prompts.split(",")]
     if min(lens) < 1 or args.steps < 1 or len(lens) > w4.GEMV_MAX_M:
@@ -139,14 +194,41 @@ def main(argv=None):
                 f"{w4.GEMV_MAX_M} sequences")
     model = Decoder(Shape(layers=args.layers, window=args.window))
     # (+ 4: the steps that warm up and record the graph)
-    cache = Cache(model.shape, [n + args.steps + 4 for n in lens], "cuda")
+    ends = [n + args.steps + 4 for n in lens]
     x = torch.randn(sum(lens), model.shape.hidden, device="cuda").bfloat16()
     begin, mid, end = (torch.cuda.Event(enable_timing=True) for _ in range(3))
+    if args.system > 0:
+        size = model.shape.page_size
+        pages = sum(-(-(args.system % size + n) // size) for n in ends) + -(-args.system // size)
+        cache = SharedCache(model.shape, len(lens), pages, args.system + max(ends), "cuda")
 
-    model.prompts(x, lens, cache)  # the first pass loads the kernels
-    cache.kv_len.zero_()
+        def tokens(*counts):
+            return torch.tensor(counts, dtype=torch.int32, device="cuda")
+
+        model.shared_pass(torch.randn(args.system, model.shape.hidden, device="cuda").bfloat16(),
+                          tokens(*[0] * len(lens), args.system), cache)
+        for b in range(len(lens)):
+            cache.share(b)
+        one_each = tokens(*[1] * len(lens), 0)
+
+        def prompts():
+            return model.shared_pass(x, tokens(*lens, 0), cache)
+
+        def step(token):
+            return model.shared_pass(token, one_each, cache)
+    else:
+        cache = Cache(model.shape, ends, "cuda")
+
+        def prompts():
+            return model.prompts(x, lens, cache)
+
+        def step(token):
+            return model.step(token, cache)
+
+        prompts()  # the first pass loads the kernels
+        cache.kv_len.zero_()
     begin.record()
-    y = model.prompts(x, lens, cache)
+    y = prompts()
     mid.record()
     torch.cuda.synchronize()
     print(f"{sum(lens)} prompt tokens in {begin.elapsed_time(mid):.3f} ms", flush=True)
@@ -155,11 +237,11 @@ def main(argv=None):
     side = torch.cuda.Stream()
     with torch.cuda.stream(side):
         side.wait_stream(torch.cuda.default_stream())
-        token.copy_(model.step(token, cache))
+        token.copy_(step(token))
         side.synchronize()
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph, stream=side):
-            token.copy_(model.step(token, cache))
+            token.copy_(step(token))
     torch.cuda.default_stream().wait_stream(side)
     graph.replay()
     begin.record()

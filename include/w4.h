@@ -480,8 +480,8 @@ size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cac
  *   len         int32 [n_prefixes]: keys of each prefix; below 0 as 0, above table_cols * page_size
  *               as that
  *   n_prefixes  1 .. W4_MAX_PREFIXES;  table_cols * page_size up to 2^30
- * The other arguments are those of w4_attn_prefill.  Limits (W4_ERR_RANGE): T <= 2^21, T * n_heads <
- * 2^26, table_cols * page_size of either table up to 2^26, and n_kv_heads (T G / 64 + n_seqs +
+ * The other arguments are those of w4_attn_prefill.  Limits (W4_ERR_RANGE): T <= 2^21, n_seqs <=
+ * 2^16, T * n_heads < 2^26, table_cols * page_size of either table up to 2^26, and n_kv_heads (T G / 64 + n_seqs +
  * n_prefixes) times the 32-key tiles that either table's pages can hold below 2^29, for G = n_heads /
  * n_kv_heads.  The softmax weights enter the second product as bf16 (up to 16 rows over the same keys: as
  * two bf16 values), their sum in fp32; partial results are fp32 in `work` and joined in a fixed order.
@@ -509,8 +509,7 @@ size_t w4_attn_shared_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cach
  *   cache    keys and values of the encoder's states; a dense [n_seqs][length][n_kv_heads][head_dim]
  *            is a cache of pages in ascending order
  *   the other arguments as for w4_attn_prefill.  A sequence without states gives y = 0, lse = -inf.
- * Limits (W4_ERR_RANGE): those of w4_attn_decode, w4_attn_shared or w4_attn_prefill, for single rows, up
- * to 16 rows a sequence and key-value head on average, and more.
+ * Limits (W4_ERR_RANGE): those of w4_attn_decode without q_start, else those of w4_attn_prefill.
  */
 int w4_attn_cross(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,
                   const w4_kv_cache *cache, float scale, void *y, int64_t ldy, int out_dtype,

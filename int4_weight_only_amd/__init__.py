@@ -674,44 +674,60 @@ def w4_attn_prefill_work_bytes(T, n_heads, k_cache, v_cache, page_table, kv_len,
 
 def _prefixes(prefix_of, prefix_table, prefix_len, n_seqs, dev):
     """The ABI's view of the prefixes of n_seqs sequences."""
-    _need(prefix_of, "prefix_of", torch.int32, dev, 1)
-    _need(prefix_table, "prefix_table", torch.int32, dev, 2)
-    _need(prefix_len, "prefix_len", torch.int32, dev, 1)
-    n, cols = prefix_table.shape
-    if prefix_of.shape[0] != n_seqs:
+    if not (prefix_of.dtype is prefix_table.dtype is prefix_len.dtype is torch.int32
+            and prefix_of.device == prefix_table.device == prefix_len.device == dev):
+        _need(prefix_of, "prefix_of", torch.int32, dev)
+        _need(prefix_table, "prefix_table", torch.int32, dev)
+        _need(prefix_len, "prefix_len", torch.int32, dev)
+    try:
+        n, cols = prefix_table.shape
+        n_of, = prefix_of.shape
+        n_lens, = prefix_len.shape
+    except ValueError:
+        raise ValueError("prefix_table must have 2 dims, prefix_of and prefix_len 1") from None
+    if n_of != n_seqs:
         raise ValueError(f"prefix_of must have {n_seqs} elements")
-    if prefix_len.shape[0] != n:
+    if n_lens != n:
         raise ValueError(f"prefix_len must have {n} elements")
+    ld, one = prefix_table.stride()
+    if (one != 1 and cols > 1) or (n_of > 1 and prefix_of.stride(0) != 1) or (
+            n > 1 and prefix_len.stride(0) != 1):
+        raise ValueError("prefix_of, prefix_table and prefix_len must be contiguous along their "
+                         "last dim")
     return _Prefixes(prefix_of.data_ptr(), prefix_table.data_ptr(), prefix_len.data_ptr(), n, cols,
-                     prefix_table.stride(0) if n > 1 else cols)
+                     ld if n > 1 else cols)
 
 
-def _rows_attention(name, q, cache, prefixes, q_start, scale, mask, out_dtype, out, want_lse, work):
+def _rows_attention(name, fn, work_bytes, q, cache, prefixes, q_start, scale, mask, out_dtype, out,
+                    want_lse, work):
     """w4_attn_shared, or w4_attn_cross where there are no prefixes (and no mask)."""
     dev = q.device
     T, width = q.shape
     D = cache.head_dim
-    if width % D != 0:
+    n_heads, odd = divmod(width, D)
+    if odd:
         raise ValueError(f"q has {width} columns, not a multiple of head_dim={D}")
     if q_start is not None:
         _need_q_start(q_start, cache.n_seqs, dev)
     elif T != cache.n_seqs:
         raise ValueError(f"q must have one row for each of {cache.n_seqs} sequences")
-    n_heads = width // D
     views = [ctypes.byref(x) for x in (cache, prefixes) if x is not None]
-    need = getattr(_lib, name + "_work_bytes")(T, n_heads, *views, *mask)
+    need = 0
     if work is None:
+        need = work_bytes(T, n_heads, *views, *mask)
         if need:
             work = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         _need(work, "work", torch.uint8, dev, 1)
+        need = work.numel()
     out = _out(out, T, width, torch.float32 if out_dtype == W4_OUT_F32 else torch.bfloat16, dev)
     lse = torch.empty((T, n_heads), dtype=torch.float32, device=dev) if want_lse else None
-    _check(name, getattr(_lib, name)(
+    status = fn(
         q.data_ptr(), T, q.stride(0) if T > 1 else width, n_heads, _ptr(q_start), *views,
         D ** -0.5 if scale is None else scale, *mask, out.data_ptr(),
-        out.stride(0) if T > 1 else width, out_dtype, _ptr(lse), _ptr(work),
-        0 if work is None else work.numel(), _stream(dev)))
+        out.stride(0) if T > 1 else width, out_dtype, _ptr(lse), _ptr(work), need, _stream(dev))
+    if status:
+        _check(name, status)
     return (out, lse) if want_lse else out
 
 
@@ -726,8 +742,9 @@ def w4_attn_shared(q, k_cache, v_cache, page_table, kv_len, prefix_of, prefix_ta
     _need(q, "q", torch.bfloat16, dim=2)
     cache = _kv_cache(k_cache, v_cache, page_table, kv_len, q.device)
     prefixes = _prefixes(prefix_of, prefix_table, prefix_len, cache.n_seqs, q.device)
-    return _rows_attention("w4_attn_shared", q, cache, prefixes, q_start, scale, (window, sinks),
-                           out_dtype, out, want_lse, work)
+    return _rows_attention("w4_attn_shared", _lib.w4_attn_shared, _lib.w4_attn_shared_work_bytes, q,
+                           cache, prefixes, q_start, scale, (window, sinks), out_dtype, out,
+                           want_lse, work)
 
 
 def w4_attn_cross(q, k_cache, v_cache, page_table, kv_len, q_start=None, scale=None,
@@ -738,8 +755,8 @@ def w4_attn_cross(q, k_cache, v_cache, page_table, kv_len, q_start=None, scale=N
     w4_attn_prefill; work: at least w4_attn_cross_work_bytes bytes."""
     _need(q, "q", torch.bfloat16, dim=2)
     cache = _kv_cache(k_cache, v_cache, page_table, kv_len, q.device)
-    return _rows_attention("w4_attn_cross", q, cache, None, q_start, scale, (), out_dtype, out,
-                           want_lse, work)
+    return _rows_attention("w4_attn_cross", _lib.w4_attn_cross, _lib.w4_attn_cross_work_bytes, q,
+                           cache, None, q_start, scale, (), out_dtype, out, want_lse, work)
 
 
 def w4_attn_shared_work_bytes(T, n_heads, k_cache, v_cache, page_table, kv_len, prefix_of,
@@ -777,19 +794,26 @@ def w4_batch_tables(kv_len, n_new, spans, page_table, page_size, ring, ring_stat
     n_seqs, cols = page_table.shape
     if kv_len.shape[0] != n_seqs or n_new.shape[0] != n_seqs:
         raise ValueError(f"kv_len and n_new must have {n_seqs} elements")
-    if tuple(spans.shape) != (n_seqs, 2) or not spans.is_contiguous():
+    if spans.shape != (n_seqs, 2) or not spans.is_contiguous():
         raise ValueError(f"spans must be contiguous [{n_seqs}][2]")
     if ring_state.shape[0] != 3:
         raise ValueError("ring_state must have 3 elements")
-    q_start = torch.empty(n_seqs + 1, dtype=torch.int32, device=dev)
+    if T < 0:
+        raise ValueError("T must not be negative")
+    # (one allocation for what is small; rows of a multiple of 16 bytes)
     slots = torch.empty(T, dtype=torch.int64, device=dev)
-    seqs, positions = torch.empty((2, T), dtype=torch.int32, device=dev).unbind()
-    if not in_place:
-        kv_out = torch.empty(n_seqs, dtype=torch.int32, device=dev)
-        spans_out = torch.empty((n_seqs, 2), dtype=torch.int32, device=dev)
-        state_out = torch.empty(3, dtype=torch.int32, device=dev)
-    else:
+    rows = (T + 3) // 4 * 4
+    if in_place:
+        seqs, positions, q_start = torch.empty(2 * rows + n_seqs + 1, dtype=torch.int32,
+                                               device=dev).split((rows, rows, n_seqs + 1))
         kv_out, spans_out, state_out = kv_len, spans, ring_state
+    else:
+        seqs, positions, q_start, kv_out, spans_out, state_out = torch.empty(
+            2 * rows + 4 * n_seqs + 4, dtype=torch.int32, device=dev).split(
+                (rows, rows, n_seqs + 1, n_seqs, 2 * n_seqs, 3))
+        spans_out = spans_out.view(n_seqs, 2)
+    if rows != T:
+        seqs, positions = seqs[:T], positions[:T]
     _check("w4_batch_tables", _lib.w4_batch_tables(
         kv_len.data_ptr(), n_new.data_ptr(), spans.data_ptr(), n_seqs, page_table.data_ptr(), cols,
         page_table.stride(0) if n_seqs > 1 else cols, page_size, ring.data_ptr(), ring.shape[0],

@@ -71,6 +71,8 @@ struct Sequence {
     __device__ __forceinline__ int prefix() const { return (packed & 511) - 1; }
 };
 constexpr int kMostTokens = 1 << 21;
+// (a worker looks through a bucket of them for each unit)
+constexpr int kMostSequences = 1 << 16;
 __device__ __forceinline__ Sequence sequence(const UnitArgs &s, int b) {
     const AttnArgs &a = s.a;
     Sequence r;
@@ -325,7 +327,7 @@ struct Units {
         const int pieces = at.whole ? workers - my_units : workers;
         const int least = (narrow ? kNarrowLeast : kWideLeast) +
                           (at.whole ? 0 : narrow ? kNarrowStart : kWideStart);
-        at.span = uniform(max(divide(my_cost, max(pieces, 1)) + 1, least));
+        at.span = uniform(max((my_cost + max(pieces, 1) - 1) / max(pieces, 1), least));
         // Lengths, and their sums: two entries of a thread.
         if (tid < n_prefixes) line.upto[tid] = lengths(at, narrow, shared_rows, shared_tiles);
         if (tid < buckets) {
@@ -773,7 +775,8 @@ int grid_of() { return 2 * device_cu_count(); }
 // The line's length: units, times the tiles that a unit can have, at the highest cost: in 31 bits.
 bool supported(int64_t T, int n_heads, const KvView &c, int n_prefixes, int prefix_capacity) {
     const int64_t G = n_heads / c.n_kv;
-    if (T > kMostTokens || T * n_heads > static_cast<int64_t>(kMaxThreads) / kWave - 4)
+    if (T > kMostTokens || c.n_seqs > kMostSequences ||
+        T * n_heads > static_cast<int64_t>(kMaxThreads) / kWave - 4)
         return false;  // (the join's waves)
     const int64_t wide = 2 * (T * G / kTileRows), groups = c.n_seqs + std::min(c.n_seqs, n_prefixes);
     const int64_t keys = std::max(c.capacity, prefix_capacity);
@@ -825,12 +828,13 @@ hipError_t launch_attn_shared(const AttnArgs &a, const KvView &c, const Prefixes
 enum CrossForm { kSingle, kUnits, kPrompts };
 CrossForm cross_form(int64_t T, int n_heads, const KvView &c, bool single) {
     if (single) return kSingle;
-    return T * (n_heads / c.n_kv) > c.n_seqs * int64_t{kNarrowRows} ? kPrompts : kUnits;
+    const bool few = T * (n_heads / c.n_kv) <= c.n_seqs * int64_t{kNarrowRows};
+    return few && supported(T, n_heads, c, 0, 0) ? kUnits : kPrompts;
 }
 bool attn_cross_supported(int64_t T, int n_heads, const KvView &c, bool single) {
     switch (cross_form(T, n_heads, c, single)) {
         case kSingle: return attn_decode_supported(n_heads, c, 0, 0);
-        case kUnits: return supported(T, n_heads, c, 0, 0);
+        case kUnits: return true;
         default: return attn_prefill_supported(T, n_heads, c, 0, 0);
     }
 }

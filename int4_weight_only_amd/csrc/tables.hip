@@ -3,7 +3,7 @@
 //
 // Three sums run over the sequences: token rows before a sequence (q_start), pages given out before
 // it, pages that came back before it. They are taken by every workgroup for itself, 1024 sequences
-// at a time (four of 256 threads each), so that one launch does: what a workgroup then needs of a
+// at a time (up to four a thread), so that one launch does: what a workgroup then needs of a
 // sequence lies in LDS. The rows, the new table entries and the pages that come back are numbered
 // through, each thread finds the sequence of its number by bisection, and the workgroups share the
 // numbers out.
@@ -18,7 +18,7 @@ namespace w4 {
 namespace {
 
 constexpr int kThreads = 256, kPerThread = 4, kChunk = kThreads * kPerThread;
-constexpr int kRowsAtOnce = 4;  // consecutive rows of a thread: its stores are 16 bytes and more
+constexpr int kAtOnce = 4;  // items of a thread, their searches and loads in flight together
 constexpr int kMostTokens = (1 << 30) - 1;
 
 struct Sums {
@@ -58,19 +58,6 @@ __device__ __forceinline__ int wave_scan_upto(int v, int T) {
     return v;
 }
 
-// The last of n ascending numbers that is at most x (the first one is).
-__device__ __forceinline__ int find(const int *first, int n, int x) {
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first[mid] <= x)
-            lo = mid;
-        else
-            hi = mid - 1;
-    }
-    return lo;
-}
-
 // FILL: rows, table entries and ring places; LENGTHS: what a sequence and the ring have afterwards.
 enum { kFill = 1, kLengths = 2 };
 
@@ -84,25 +71,22 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(TablesArgs a, in
     const int head = a.ring_state[0] >= 0 && a.ring_state[0] < R ? a.ring_state[0] : 0;
     const bool lengths = (what & kLengths) && blockIdx.x == 0;
     const bool fill = (what & kFill) != 0;
-    const int start = blockIdx.x * kThreads + tid, step = gridDim.x * kThreads;
-    // the page of number k among those given out, -1 where the ring holds no more
-    const auto given = [&](int k) {
-        if (k >= count) return -1;
-        const int at = head + k;
-        return a.ring[at >= R ? at - R : at];
-    };
+    const int start = blockIdx.x * kThreads * kAtOnce + tid, step = gridDim.x * kThreads * kAtOnce;
+    // the ring's place of number k from its head on
+    const auto place_of = [&](int64_t k) { return head + k >= R ? head + k - R : head + k; };
 
     Sums before = {0, 0, 0};
     if (lengths && tid == 0) a.q_start[0] = 0;
     for (int base = 0; base < a.n_seqs; base += kChunk) {
         const int n = min(a.n_seqs - base, kChunk);
         // the sequences of a thread follow each other
+        const int each = (n + kThreads - 1) / kThreads;
         Request r[kPerThread];
         Sums mine = {0, 0, 0};
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
-            const int b = base + tid * kPerThread + i;
-            if (b < a.n_seqs) {
+            const int b = base + tid * each + i;
+            if (i < each && b < a.n_seqs) {
                 r[i] = request(a, b);
                 mine.rows = min(mine.rows + min(r[i].tokens, T), T);
                 mine.fresh += r[i].fresh();
@@ -130,8 +114,8 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(TablesArgs a, in
         }
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) {
-            const int place = tid * kPerThread + i, b = base + place;
-            if (b < a.n_seqs) {
+            const int place = tid * each + i, b = base + place;
+            if (i < each && b < a.n_seqs) {
                 s_row[place] = at.rows;
                 s_fresh[place] = at.fresh;
                 s_back[place] = at.back;
@@ -153,40 +137,85 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(TablesArgs a, in
         }
         __syncthreads();
         if (fill) {
-            // new table entries
-            for (int k = before.fresh + start; k < all.fresh; k += step) {
-                const int p = find(s_fresh, n, k);
-                a.page_table[(base + p) * a.ld_table + s_end[p] + k - s_fresh[p]] = given(k);
-            }
-            // pages that come back, behind those of the ring
-            for (int k = before.back + start; k < all.back && k < R - count; k += step) {
-                const int p = find(s_back, n, k);
-                const int64_t to = static_cast<int64_t>(head) + count + k;
-                a.ring[to >= R ? to - R : to] =
-                    a.page_table[(base + p) * a.ld_table + s_begin[p] + k - s_back[p]];
-            }
-            // rows
-            for (int t = before.rows + start; t < all.rows; t += step) {
-                const int p = find(s_row, n, t);
-                const int pos = s_len[p] + t - s_row[p], col = pos >> a.page_shift;
-                int page = -1;
-                if (col < s_end[p])
-                    page = a.page_table[(base + p) * a.ld_table + col];
-                else if (col < a.table_cols)
-                    page = given(s_fresh[p] + col - s_end[p]);
-                if (a.slots)
-                    a.slots[t] = page < 0 ? -1
-                                          : (static_cast<int64_t>(page) << a.page_shift) +
-                                                (pos & ((1 << a.page_shift) - 1));
-                if (a.seqs) a.seqs[t] = base + p;
-                if (a.positions) a.positions[t] = pos;
+            // The items of these sequences: new table entries, pages that come back, rows; each takes
+            // one page from the table or the ring.
+            const int fresh = all.fresh - before.fresh;
+            const int back = max(min(all.back, R - count) - before.back, 0);
+            const int items = fresh + back + all.rows - before.rows;
+            // the last sequence of p .. n - 1 with no more than k before it; steps: at least n - p
+            const auto find = [&](const int *first, int p, int bit, int k) {
+                const int at = min(p + bit, n - 1);
+                return first[at] <= k ? at : p;
+            };
+            for (int j0 = start; j0 - tid < items; j0 += step) {
+                // Where the workgroup's items are all rows, they belong to few sequences.
+                int from = 0, bits = n;
+                const int rows0 = fresh + back, c0 = j0 - tid;
+                if (c0 >= rows0) {
+                    const int k0 = before.rows + c0 - rows0;
+                    const int k1 = min(k0 + kThreads * kAtOnce, all.rows) - 1;
+                    int last = 0;
+                    for (int bit = 1 << (31 - __builtin_clz(n)); bit > 0; bit >>= 1) {
+                        from = find(s_row, from, bit, k0);
+                        last = find(s_row, last, bit, k1);
+                    }
+                    bits = last - from;
+                }
+                int kind[kAtOnce], k[kAtOnce], p[kAtOnce], page[kAtOnce];
+                const int *first[kAtOnce];
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int j = min(j0 + i * kThreads, items - 1);
+                    kind[i] = j < fresh ? 0 : j < fresh + back ? 1 : 2;
+                    k[i] = kind[i] == 0   ? before.fresh + j
+                           : kind[i] == 1 ? before.back + j - fresh
+                                          : before.rows + j - fresh - back;
+                    first[i] = kind[i] == 0 ? s_fresh : kind[i] == 1 ? s_back : s_row;
+                    p[i] = from;
+                }
+                for (int bit = bits > 0 ? 1 << (31 - __builtin_clz(bits)) : 0; bit > 0; bit >>= 1)
+#pragma unroll
+                    for (int i = 0; i < kAtOnce; ++i) p[i] = find(first[i], p[i], bit, k[i]);
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    const int b = base + p[i], end = s_end[p[i]], in = k[i] - first[i][p[i]];
+                    const int col = kind[i] == 1 ? s_begin[p[i]] + in
+                                                 : (s_len[p[i]] + in) >> a.page_shift;
+                    // number among the pages given out, of a new entry or a row on one
+                    const int number = kind[i] == 0 ? k[i] : s_fresh[p[i]] + col - end;
+                    const bool held = kind[i] == 1 || (kind[i] == 2 && col < end);
+                    page[i] = -1;
+                    if (held)
+                        page[i] = a.page_table[b * a.ld_table + col];
+                    else if (number < count && (kind[i] == 0 || col < a.table_cols))
+                        page[i] = a.ring[place_of(number)];
+                }
+#pragma unroll
+                for (int i = 0; i < kAtOnce; ++i) {
+                    if (j0 + i * kThreads >= items) break;
+                    const int b = base + p[i], in = k[i] - first[i][p[i]];
+                    if (kind[i] == 0) {
+                        a.page_table[b * a.ld_table + s_end[p[i]] + in] = page[i];
+                    } else if (kind[i] == 1) {
+                        a.ring[place_of(static_cast<int64_t>(count) + k[i])] = page[i];
+                    } else {
+                        const int pos = s_len[p[i]] + in;
+                        if (a.slots)
+                            a.slots[k[i]] = page[i] < 0
+                                                ? -1
+                                                : (static_cast<int64_t>(page[i]) << a.page_shift) +
+                                                      (pos & ((1 << a.page_shift) - 1));
+                        if (a.seqs) a.seqs[k[i]] = b;
+                        if (a.positions) a.positions[k[i]] = pos;
+                    }
+                }
             }
         }
         before = all;
         __syncthreads();
     }
     if (fill) {
-        for (int t = before.rows + start; t < T; t += step) {
+        for (int t = before.rows + blockIdx.x * kThreads + tid; t < T; t += gridDim.x * kThreads) {
             if (a.slots) a.slots[t] = -1;
             if (a.seqs) a.seqs[t] = -1;
             if (a.positions) a.positions[t] = -1;
