@@ -632,7 +632,30 @@ __device__ __forceinline__ int attn_tile(const typename Rows::Args &args,
         }
         return t.next;
     }
-    if (n_iter > 0) {
+    bool again = false;
+    // (with few rows in a unit, waves without any only move keys and values, at the same barriers)
+    const bool idle = TABLES && !__any(t.live);
+    if (idle && n_iter > 0) {
+        look_up(0);
+        locate(0, newest);
+        fetch(head_k, newest, k_col, sk0, L::kKeyBlock);
+        phase_fence();
+        look_up(tile_at(1));
+        send(-1, sk1, sv0);
+        phase_fence();
+        __builtin_amdgcn_s_waitcnt(wait_vm<2 * kLoads>());
+        __builtin_amdgcn_s_barrier();
+        phase_fence();
+        tile_barrier();
+        for (int it = 0; it + 1 < n_iter; ++it) {
+            if (it & 1)
+                send(it, sk1, sv0);
+            else
+                send(it, sk0, sv1);
+            tile_barrier();
+        }
+    }
+    if (!idle && n_iter > 0) {
         look_up(0);
         locate(0, newest);
         fetch(head_k, newest, k_col, sk0, L::kKeyBlock);
@@ -668,15 +691,15 @@ __device__ __forceinline__ int attn_tile(const typename Rows::Args &args,
         for (int d = 0; d < DT; ++d)
 #pragma unroll
             for (int i = 0; i < 16; ++i) odd[i % 4] = fmaf(o[d][i], 0.0f, odd[i % 4]);
-        const bool again = odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f || is_far();
-        if (__builtin_expect(block_any(again), 0)) {
-            attn_tile<Rows, DP, KT, PAGES, true>(args_again<typename Rows::Args>(), state, sk0, sk0,
-                                                 sv0, sv0, votes);
-            return t.next;
-        }
+        again = odd[0] + odd[1] + (odd[2] + odd[3]) != 0.0f || is_far();
+    }
+    if (n_iter > 0 && __builtin_expect(block_any(again), 0)) {
+        attn_tile<Rows, DP, KT, PAGES, true>(args_again<typename Rows::Args>(), state, sk0, sk0, sv0,
+                                             sv0, votes);
+        return t.next;
     }
 
-    write(true, 0, std::integral_constant<int, DT>{}, o);
+    if (!idle) write(true, 0, std::integral_constant<int, DT>{}, o);
     return t.next;
 }
 
