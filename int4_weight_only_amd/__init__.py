@@ -784,41 +784,52 @@ def w4_batch_tables(kv_len, n_new, spans, page_table, page_size, ring, ring_stat
 
     Returns (q_start int32 [n_seqs + 1], slots int64 [T], seqs int32 [T], positions int32 [T],
     kv_len, spans, ring_state), the last three new tensors, or with in_place those given."""
-    _need(kv_len, "kv_len", torch.int32, dim=1)
+    arrays = (kv_len, n_new, spans, page_table, ring, ring_state)
     dev = kv_len.device
-    _need(n_new, "n_new", torch.int32, dev, 1)
-    _need(spans, "spans", torch.int32, dev, 2)
-    _need(page_table, "page_table", torch.int32, dev, 2)
-    _need(ring, "ring", torch.int32, dev, 1)
-    _need(ring_state, "ring_state", torch.int32, dev, 1)
-    n_seqs, cols = page_table.shape
-    if kv_len.shape[0] != n_seqs or n_new.shape[0] != n_seqs:
+    if not (kv_len.dtype is n_new.dtype is spans.dtype is page_table.dtype is ring.dtype
+            is ring_state.dtype is torch.int32 and kv_len.is_cuda
+            and dev == n_new.device == spans.device == page_table.device == ring.device
+            == ring_state.device):
+        for name, t in zip(("kv_len", "n_new", "spans", "page_table", "ring", "ring_state"), arrays):
+            _need(t, name, torch.int32, dev)
+    try:
+        n_seqs, cols = page_table.shape
+        ld, one = page_table.stride()
+        (n_lens,), (n_tokens,), (n_spans, two), (places,), (words,) = (
+            kv_len.shape, n_new.shape, spans.shape, ring.shape, ring_state.shape)
+    except ValueError:
+        raise ValueError("page_table and spans must have 2 dims, the other arrays 1") from None
+    if n_lens != n_seqs or n_tokens != n_seqs:
         raise ValueError(f"kv_len and n_new must have {n_seqs} elements")
-    if spans.shape != (n_seqs, 2) or not spans.is_contiguous():
-        raise ValueError(f"spans must be contiguous [{n_seqs}][2]")
-    if ring_state.shape[0] != 3:
+    if n_spans != n_seqs or two != 2:
+        raise ValueError(f"spans must be [{n_seqs}][2]")
+    if words != 3:
         raise ValueError("ring_state must have 3 elements")
+    if (one != 1 and cols > 1) or not (kv_len.is_contiguous() and n_new.is_contiguous()
+                                       and spans.is_contiguous() and ring.is_contiguous()
+                                       and ring_state.is_contiguous()):
+        raise ValueError("page_table must be contiguous along its last dim, the other arrays "
+                         "contiguous")
     if T < 0:
         raise ValueError("T must not be negative")
-    # (one allocation for what is small; rows of a multiple of 16 bytes)
+    # (few allocations: each costs a small call as much as a fifth of its kernel)
     slots = torch.empty(T, dtype=torch.int64, device=dev)
-    rows = (T + 3) // 4 * 4
     if in_place:
-        seqs, positions, q_start = torch.empty(2 * rows + n_seqs + 1, dtype=torch.int32,
-                                               device=dev).split((rows, rows, n_seqs + 1))
+        seqs, positions, q_start = torch.split_with_sizes(
+            torch.empty(2 * T + n_seqs + 1, dtype=torch.int32, device=dev), (T, T, n_seqs + 1))
         kv_out, spans_out, state_out = kv_len, spans, ring_state
     else:
-        seqs, positions, q_start, kv_out, spans_out, state_out = torch.empty(
-            2 * rows + 4 * n_seqs + 4, dtype=torch.int32, device=dev).split(
-                (rows, rows, n_seqs + 1, n_seqs, 2 * n_seqs, 3))
-        spans_out = spans_out.view(n_seqs, 2)
-    if rows != T:
-        seqs, positions = seqs[:T], positions[:T]
-    _check("w4_batch_tables", _lib.w4_batch_tables(
+        seqs, positions, q_start, kv_out, state_out = torch.split_with_sizes(
+            torch.empty(2 * T + 2 * n_seqs + 4, dtype=torch.int32, device=dev),
+            (T, T, n_seqs + 1, n_seqs, 3))
+        spans_out = torch.empty((n_seqs, 2), dtype=torch.int32, device=dev)
+    status = _lib.w4_batch_tables(
         kv_len.data_ptr(), n_new.data_ptr(), spans.data_ptr(), n_seqs, page_table.data_ptr(), cols,
-        page_table.stride(0) if n_seqs > 1 else cols, page_size, ring.data_ptr(), ring.shape[0],
-        ring_state.data_ptr(), T, q_start.data_ptr(), _ptr(slots), _ptr(seqs), _ptr(positions),
-        kv_out.data_ptr(), spans_out.data_ptr(), state_out.data_ptr(), _stream(dev)))
+        ld if n_seqs > 1 else cols, page_size, ring.data_ptr(), places, ring_state.data_ptr(), T,
+        q_start.data_ptr(), _ptr(slots), _ptr(seqs), _ptr(positions), kv_out.data_ptr(),
+        spans_out.data_ptr(), state_out.data_ptr(), _stream(dev))
+    if status:
+        _check("w4_batch_tables", status)
     return q_start, slots, seqs, positions, kv_out, spans_out, state_out
 
 
