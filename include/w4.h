@@ -1,7 +1,7 @@
 /*
  * w4.h -- C ABI of libw4.so: the group-wise INT4 weight-only quantized linear layer on MI355X
  * (gfx950), and the operators of a decoder layer around it (rotary positions, attention over a
- * paged key-value cache, the residual norm).
+ * paged key-value cache, cross attention, the cache's tables, the residual norm).
  *
  *   y = x . W_hat^T (+ b),   W_hat[j][k] = s[j][G] * (code[j][k] - z[j][G]),  G = k / group_size
  *
@@ -323,8 +323,8 @@ int w4a8_gemm(const int8_t *q, const float *s_x, int64_t M, int64_t ldq, const u
 
 /*
  * The operators of a decoder layer that stand between its linears: rotary positions and the append
- * to a paged key-value cache, attention of one new token and of prompts over that cache, and the
- * residual norm.  (Lab5 基础: the layer's attention with its sliding window; Infra 第四部分: the
+ * to a paged key-value cache, attention of one new token and of prompts over that cache, of sequences
+ * that share prefixes and over an encoder's states, the tables of a step, and the residual norm.  (Lab5 基础: the layer's attention with its sliding window; Infra 第四部分: the
  * paged cache of a serving batch.)
  *
  * w4_kv_cache -- a paged key-value cache and the sequences in it.  The struct is read on the host
@@ -480,11 +480,13 @@ size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cac
  *   len         int32 [n_prefixes]: keys of each prefix; below 0 as 0, above table_cols * page_size
  *               as that
  *   n_prefixes  1 .. W4_MAX_PREFIXES;  table_cols * page_size up to 2^30
- * The other arguments are those of w4_attn_prefill.  Limits (W4_ERR_RANGE): T <= 2^21, n_seqs <=
- * 2^16, T * n_heads < 2^26, table_cols * page_size of either table up to 2^26, and n_kv_heads (T G / 64 + n_seqs +
- * n_prefixes) times the 32-key tiles that either table's pages can hold below 2^29, for G = n_heads /
- * n_kv_heads.  The softmax weights enter the second product as bf16 (up to 16 rows over the same keys: as
- * two bf16 values), their sum in fp32; partial results are fp32 in `work` and joined in a fixed order.
+ * The other arguments are those of w4_attn_prefill.  Limits (W4_ERR_RANGE): T <= 2^21, n_seqs
+ * <= 2^16, T * n_heads < 2^26, table_cols * page_size of either table up to 2^26, and n_kv_heads (T G / 64
+ * + n_seqs + n_prefixes) times the 32-key tiles that either table's pages can hold below 2^29, for G =
+ * n_heads / n_kv_heads.  The softmax weights enter the second product as bf16 (up to 16 rows over the same
+ * keys: as two bf16 values), their sum in fp32; partial results are fp32 in `work`, joined in a fixed
+ * order.  work: 8 (head_dim + 4) bytes for each row and query head, and 1024 (head_dim + 2) for each
+ * compute unit.
  */
 typedef struct w4_prefixes {
     const int32_t *prefix_of, *table, *len;

@@ -18,6 +18,9 @@
 // A workgroup is four waves, 128 stacked rows; tiles of 64 keys (32 at 256 dims) go from memory
 // straight to LDS, double buffered, one barrier a tile. Two workgroups run on a compute unit, so
 // that one can multiply while the other turns scores into weights.
+//
+// Rows says which rows these are, which keys they see and where their results go: of one sequence over
+// its keys (attn_prefill.hip), or of many over keys that lie by one or two page tables (attn_units.hip).
 #pragma once
 
 #include <type_traits>
@@ -633,7 +636,9 @@ __device__ __forceinline__ int attn_tile(const typename Rows::Args &args,
         return t.next;
     }
     bool again = false;
-    // (with few rows in a unit, waves without any only move keys and values, at the same barriers)
+    // (with few rows in a unit, waves without any only move keys and values, at the same barriers: a loop
+    // of its own, as conditions inside the other one spilled its registers. 24 sequences of 5 tokens, 16
+    // heads over 4 of 256, 20 rows each: 45 us, all waves multiplying 50.)
     const bool idle = TABLES && !__any(t.live);
     if (idle && n_iter > 0) {
         look_up(0);

