@@ -324,8 +324,9 @@ int w4a8_gemm(const int8_t *q, const float *s_x, int64_t M, int64_t ldq, const u
 /*
  * The operators of a decoder layer that stand between its linears: rotary positions and the append
  * to a paged key-value cache, attention of one new token and of prompts over that cache, of sequences
- * that share prefixes and over an encoder's states, the tables of a step, and the residual norm.  (Lab5 基础: the layer's attention with its sliding window; Infra 第四部分: the
- * paged cache of a serving batch.)
+ * that share prefixes and over an encoder's states, the tables of a step, and the residual norm.
+ * (Lab5 基础: the layer's attention with its sliding window; Infra 第四部分: the paged cache of a
+ * serving batch.)
  *
  * w4_kv_cache -- a paged key-value cache and the sequences in it.  The struct is read on the host
  * during the call; its arrays are device memory.
@@ -534,9 +535,12 @@ size_t w4_attn_cross_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache
  * Free pages lie in a ring: ring_state = {head, count, missing}, number k of `count` at place
  * (head + k) % ring_size.  Pages are taken from its head; pages that come back follow its last one, in
  * the order of the sequences and of the entries.  Where no page is left the entry becomes -1 (an
- * append there is dropped), the row's slot -1, and missing_out counts those entries: the step has to
- * be made again with more free pages, from the same kv_len and spans.  Entries past the table's last
- * column are neither written nor counted; rows there get slot -1.
+ * append there is dropped), the row's slot -1, and missing_out counts those entries.  The step can then be
+ * made again from the kv_len, spans and ring_state that it had (all three: pages taken and returned are
+ * taken and returned again), after a call in which a sequence ended, or with pages put into the ring
+ * behind its last one and `count` raised.  So a caller that may run out keeps them: an output in place
+ * overwrites them.  Entries past the table's last column are neither written nor counted; rows there get
+ * slot -1.
  *   n_new        int32 [n_seqs], values up to 2^30 - 1;  spans, spans_out  int32 [n_seqs][2]
  *   kv_len, kv_len_out  int32 [n_seqs];   ring_state, ring_state_out  int32 [3]
  *   page_table   int32 [n_seqs][ld_table], table_cols entries used, in and out

@@ -783,7 +783,9 @@ def w4_batch_tables(kv_len, n_new, spans, page_table, page_size, ring, ring_stat
     count, missing).  T: token rows of the step (those behind the last sequence's get -1).
 
     Returns (q_start int32 [n_seqs + 1], slots int64 [T], seqs int32 [T], positions int32 [T],
-    kv_len, spans, ring_state), the last three new tensors, or with in_place those given."""
+    kv_len, spans, ring_state), the last three new tensors, or with in_place those given.  Where
+    ring_state[2] is above 0 after the call, that many pages were missing: the step can be made again
+    from the kv_len, spans and ring_state that it had, once there are more."""
     arrays = (kv_len, n_new, spans, page_table, ring, ring_state)
     dev = kv_len.device
     if not (kv_len.dtype is n_new.dtype is spans.dtype is page_table.dtype is ring.dtype

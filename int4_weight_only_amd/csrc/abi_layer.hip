@@ -1,7 +1,7 @@
 // abi_layer.hip -- the extern "C" entry points of the operators between a decoder layer's linears
 // (rotary positions with the cache append, the tables of a step, attention over the paged cache, the
-// residual norm): host-side argument validation and dispatch.  The contract of every entry point is stated in
-// include/w4.h; nothing here allocates device memory or synchronizes.
+// residual norm): host-side argument validation and dispatch.  The contract of every entry point is
+// stated in include/w4.h; nothing here allocates device memory or synchronizes.
 #include <hip/hip_runtime.h>
 
 #include <cmath>

@@ -544,8 +544,7 @@ def test_tables_of_long_prompts(in_place):
 
 
 def test_tables_when_pages_run_out():
-    """Entries and rows without a page are -1 and counted; they get one when the call is made again
-    with pages, from what the sequences had before."""
+    """Entries and rows without a page are -1 and counted; pages that come back serve the next call."""
     rng = np.random.default_rng(33)
     pool = Pool(rng, [30, 0, 16, 3], 10, 16, 5)
     got = tables_step(pool, [40, 50, 1, 1], 92)
@@ -556,6 +555,37 @@ def test_tables_when_pages_run_out():
     tables_step(pool, [1, 1], 2)  # the last slots of pages they have
     tables_step(pool, [-1, 40], 40)  # pages that come back serve the next call
     tables_step(pool, [0, 1], 1)
+
+
+def test_tables_of_a_step_made_again():
+    """A step that ran out is made again from the lengths, spans and ring that it had: after a call in
+    which another sequence gave up its pages, and after pages were put into the ring. No page is lost
+    or given out twice."""
+    rng = np.random.default_rng(40)
+    pool = Pool(rng, [30, 20, 0, 64, 5], 10, 16, 2)
+    n_new = [40, -1, 33, 1, 1]  # 3 + 0 + 3 + 1 + 0 pages of 2; 2 come back
+    was = [x.copy() for x in (pool.kv_len, pool.spans, pool.state)]
+    assert tables_step(pool, n_new, 75)[6].tolist()[1:] == [2, 5]
+    pool.kv_len, pool.spans, pool.state = (x.copy() for x in was)
+    tables_step(pool, [0, 0, 0, -1, 0], 0)  # 4 pages of sequence 3
+    assert pool.state.tolist()[1:] == [6, 0]
+    n_new[3] = 0
+    was = [x.copy() for x in (pool.kv_len, pool.spans, pool.state)]
+    n_new[4] = 28  # two pages more
+    assert tables_step(pool, n_new, 101)[6].tolist()[1:] == [2, 2]
+    pool.kv_len, pool.spans, pool.state = (x.copy() for x in was)
+    extra = len(pool.ring) - int(pool.state[1])
+    held = {int(pool.table[b, j]) for b in range(5) for j in range(*pool.spans[b])}
+    free = set(pool.ring[(pool.state[0] + np.arange(pool.state[1])) % len(pool.ring)].tolist())
+    assert len(free) == 6 and not free & held and extra >= 2
+    new = [1000, 1001]
+    pool.ring[(pool.state[0] + pool.state[1] + np.arange(2)) % len(pool.ring)] = new
+    pool.state[1] += 2
+    got = tables_step(pool, n_new, 101)
+    assert got[6].tolist()[2] == 0 and (got[1][:int(got[0][-1])] >= 0).all()
+    used = [int(pool.table[b, j]) for b in range(5) for j in range(*pool.spans[b])]
+    left = pool.ring[(pool.state[0] + np.arange(pool.state[1])) % len(pool.ring)].tolist()
+    assert sorted(used + left) == sorted(held | free | set(new))
 
 
 def test_tables_narrower_than_the_sequences():
