@@ -708,9 +708,10 @@ __device__ __forceinline__ int attn_tile(const typename Rows::Args &args,
     return t.next;
 }
 
-template <class Rows, int DP, int KT, int PAGES>
+// PER_CU: workgroups on a compute unit.
+template <class Rows, int DP, int KT, int PAGES, int PER_CU>
 __global__ void __launch_bounds__(kTileWaves * 64)
-__attribute__((amdgpu_waves_per_eu(2, 2))) attn_tile_kernel(typename Rows::Args args) {
+__attribute__((amdgpu_waves_per_eu(PER_CU, PER_CU))) attn_tile_kernel(typename Rows::Args args) {
     using L = TileLayout<DP>;
     // (arrays of their own: the compiler then sees that a direct load on its way into one does not
     // touch the others, and does not wait for it before it reads them)
@@ -725,28 +726,29 @@ __attribute__((amdgpu_waves_per_eu(2, 2))) attn_tile_kernel(typename Rows::Args 
 // Keys of a tile, by head size.
 constexpr int tile_keys(int head_dim) { return head_dim > 128 ? 32 : 64; }
 
-template <class Rows, int DP>
+template <class Rows, int DP, int PER_CU>
 void launch_tiles(const typename Rows::Args &args, int64_t blocks, hipStream_t stream) {
     constexpr int KT = tile_keys(DP);
-    const dim3 grid(static_cast<unsigned>(blocks)), block(kTileWaves * 64);
-    if (args.c.page_mask >= KT - 1)
-        hipLaunchKernelGGL((attn_tile_kernel<Rows, DP, KT, kTilePages>), grid, block, 0, stream,
-                           args);
-    else if (args.c.page_mask >= 7)
-        hipLaunchKernelGGL((attn_tile_kernel<Rows, DP, KT, kSpanPages>), grid, block, 0, stream,
-                           args);
-    else
-        hipLaunchKernelGGL((attn_tile_kernel<Rows, DP, KT, kAnyPages>), grid, block, 0, stream,
-                           args);
+    const auto kernel = args.c.page_mask >= KT - 1 ? attn_tile_kernel<Rows, DP, KT, kTilePages, PER_CU>
+                        : args.c.page_mask >= 7 ? attn_tile_kernel<Rows, DP, KT, kSpanPages, PER_CU>
+                                                : attn_tile_kernel<Rows, DP, KT, kAnyPages, PER_CU>;
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kTileWaves * 64), 0, stream,
+                       args);
 }
 template <class Rows>
 void launch_tiles(const typename Rows::Args &args, int64_t blocks, hipStream_t stream) {
-    if (args.c.head_dim <= 64)
-        launch_tiles<Rows, 64>(args, blocks, stream);
+    // At 64 dims registers do for three workgroups on a compute unit (those of the second pass are
+    // spilled): prompts of 3 x 4096, 28 heads over 4, 179 to 186 us for 194 to 199; 8 x 448 rows over 1500 states, 20
+    // heads, 49 for 55, as 580 workgroups then run at once. Where two on each hold all, three only
+    // share them out unevenly: 4 x 200 after 3000 keys 28.3 us for 27.3.
+    if (args.c.head_dim <= 64 && blocks > 2 * int64_t{device_cu_count()})
+        launch_tiles<Rows, 64, 3>(args, blocks, stream);
+    else if (args.c.head_dim <= 64)
+        launch_tiles<Rows, 64, 2>(args, blocks, stream);
     else if (args.c.head_dim <= 128)
-        launch_tiles<Rows, 128>(args, blocks, stream);
+        launch_tiles<Rows, 128, 2>(args, blocks, stream);
     else
-        launch_tiles<Rows, 256>(args, blocks, stream);
+        launch_tiles<Rows, 256, 2>(args, blocks, stream);
 }
 
 }  // namespace w4

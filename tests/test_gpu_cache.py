@@ -399,6 +399,51 @@ def test_cross_few_rows_over_many_states_and_the_reverse():
             2, 1, 32, 16, extra=1)
 
 
+# sequences whose rows make more workgroups than two for each of 256 compute units, with 16 heads
+MANY_ROWS = [500, 300, 0, 431, 17, 640, 129, 128, 350, 700]
+MANY_KEYS = [77, 130, 50, 64, 200, 1, 300, 0, 65, 128]
+
+
+@pytest.mark.parametrize("D,page", [(64, 64), (64, 16), (64, 4), (40, 64), (32, 8)])
+def test_cross_of_many_rows_at_small_head_sizes(D, page):
+    crossed(np.random.default_rng([24, D, page]), MANY_KEYS, MANY_ROWS, 16, 16, D, page, extra=3)
+
+
+@pytest.mark.parametrize("page", [64, 16, 4])
+@pytest.mark.parametrize("call", [w4.w4_attn_cross, w4.w4_attn_prefill])
+@pytest.mark.parametrize("case", ["plain", "far", "inf"])
+def test_many_rows_agree_with_each_sequence_alone(call, page, case):
+    """A batch of many workgroups at 64 dims against calls of few, bit for bit; with scores far from 0
+    and values that are not finite too, which take a second pass."""
+    rng = np.random.default_rng([25, page])
+    H, D = 16, 64
+    lens = [max(n, m) + 20 for n, m in zip(MANY_KEYS, MANY_ROWS)]
+    lens = [min(n, 448) for n in lens]
+    rows = [min(m, n) for m, n in zip(MANY_ROWS, lens)]
+    rows[4] = 400
+    lens[4] = 440
+    batch = Batch(rng, [0], [-1] * len(lens), lens, page, H, D, cols=448 // page)
+    starts = np.concatenate([[0], np.cumsum(rows)])
+    assert (starts[-1] // 128 + len(rows)) * H > 512
+    batch.fill(rng, seen_slots(batch, starts, 0, 0, True), 1e18 if case == "far" else 1.0)
+    if case == "inf":
+        for b, pos, value in ((0, 5, float("inf")), (3, 60, float("nan")), (9, 100, -float("inf"))):
+            slot = int(batch.at[b][pos])
+            batch.v[slot // page, slot % page, 3, 7:40] = value
+    q = bf16(2.0 * rng.normal(size=(starts[-1], H * D))).cuda()
+    k, v, table, kv_len = batch.args()
+    y = call(q, k, v, table, kv_len, ints(starts), out_dtype=w4.W4_OUT_F32)
+    for b in range(len(rows)):
+        one = slice(int(starts[b]), int(starts[b + 1]))
+        if rows[b] == 0:
+            continue
+        alone = call(q[one], k, v, table[b:b + 1], kv_len[b:b + 1], ints([0, rows[b]]),
+                     out_dtype=w4.W4_OUT_F32)
+        assert torch.equal(torch.nan_to_num(alone, nan=12345.0), torch.nan_to_num(y[one], nan=12345.0))
+        if case == "inf":
+            assert torch.isfinite(alone).all() == (b not in (0, 3, 9))
+
+
 def test_cross_over_a_dense_array_of_states():
     """[B][length][heads][D] seen as pages in order; rows of one sequence are independent beams."""
     rng = np.random.default_rng(24)
