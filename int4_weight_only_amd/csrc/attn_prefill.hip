@@ -31,9 +31,11 @@ struct Tile {
 
 // Tiles of BM rows of all sequences in the order in which they are given out: the tiles that see
 // most keys first (by their level: the tile's number in its sequence plus the tiles its earlier
-// keys would make), so that the last ones to run are short. Up to 64 sequences, a lane each; more
-// are taken in order, the last rows of each first. Every lane of every wave takes part.
-template <int BM>
+// keys would make), so that the last ones to run are short. With CROSS every tile of a sequence sees
+// all of its keys, which are its level (2 x 2000 rows over 6000 states 336 us for 350, 28 heads over 4
+// of 128). Up to 64 sequences, a lane each; more are taken in order, the last rows of each first. Every
+// lane of every wave takes part.
+template <int BM, bool CROSS>
 __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_start, int64_t T,
                                           int G, int tile, Tile *out) {
     const int lane = threadIdx.x & (kWave - 1);
@@ -55,26 +57,31 @@ __device__ __forceinline__ bool find_tile(const KvView &c, const int32_t *q_star
         }
         int w, row_tile;  // the lane of the sequence, the tile's number in it
         if (c.n_seqs <= kWave) {
-            // levels first .. first + mine - 1 are this sequence's; the largest level with more
-            // than `tile` tiles at it or above
-            const int first = static_cast<int>(
-                min(static_cast<int64_t>(max(n_keys - nq, 0)) * G / BM, int64_t{1} << 29));
-            int lo = 0, hi = wave_max_dpp(first + mine);
+            // levels first .. first + mine - 1 are this sequence's (CROSS: `first`, of 64 keys each);
+            // the largest level with more than `tile` tiles at it or above
+            const int first =
+                CROSS ? n_keys >> 6
+                      : static_cast<int>(min(static_cast<int64_t>(max(n_keys - nq, 0)) * G / BM,
+                                             int64_t{1} << 29));
+            const auto from_level = [&](int level) {  // this sequence's tiles at it or above
+                return CROSS ? (first >= level ? mine : 0) : max(min(first + mine - level, mine), 0);
+            };
+            int lo = 0, hi = wave_max_dpp(CROSS ? first : first + mine);
             while (lo < hi) {
                 const int mid = lo + (hi - lo + 1) / 2;
-                const int above = max(min(first + mine - mid, mine), 0);
-                if (wave_sum_dpp(above) > tile)
+                if (wave_sum_dpp(from_level(mid)) > tile)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
-            const int above = wave_sum_dpp(max(min(first + mine - (lo + 1), mine), 0));
-            const int here = (first <= lo) & (lo < first + mine);
-            const int rank = wave_scan_dpp(here);  // (with every lane: outside of any condition)
-            const uint64_t hit = __ballot((here != 0) & (rank == tile - above + 1));
+            const int above = wave_sum_dpp(from_level(lo + 1));
+            const int here = from_level(lo) - from_level(lo + 1);
+            const int upto = wave_scan_dpp(here);  // (with every lane: outside of any condition)
+            const uint64_t hit = __ballot((here != 0) & (above + upto > tile));
             if (!hit) return false;
             w = __builtin_ctzll(hit);
-            row_tile = lo - __builtin_amdgcn_readlane(first, w);
+            row_tile = CROSS ? tile - above - __builtin_amdgcn_readlane(upto - here, w)
+                             : lo - __builtin_amdgcn_readlane(first, w);
         } else {
             const uint64_t hit = __ballot(before + sum > tile);
             if (!hit) return false;
@@ -125,7 +132,7 @@ struct PrefillRows {
         r->part_end = r->part + 1;
         r->parts = args.splits;
         Tile t;
-        if (!find_tile<kTileRows>(c, a.q_start, a.T, G, blockIdx.x / c.n_kv / args.splits, &t))
+        if (!find_tile<kTileRows, CROSS>(c, a.q_start, a.T, G, blockIdx.x / c.n_kv / args.splits, &t))
             return false;
         const int row = t.row0 + wid * 32 + (lane & 31);
         const int safe_row = min(row, t.rows - 1);
