@@ -843,7 +843,7 @@ hipError_t launch_attn_shared(const AttnArgs &a, const KvView &c, const Prefixes
 
 // Cross attention: single rows as a decode step, sequences of up to 16 rows as units, of more as prompts
 // (which have most pieces' sums nowhere to write: 2 x 2000 rows over 6000 states, 28 heads over 4 of 128,
-// 354 us for 385 as units; 16 x 5 rows over up to 1500, 20 heads of 64, 28 us as units for 36).
+// 336 us for 385 as units; 16 x 5 rows over up to 1500, 20 heads of 64, 28 us as units for 36).
 enum CrossForm { kSingle, kUnits, kPrompts };
 CrossForm cross_form(int64_t T, int n_heads, const KvView &c, bool single) {
     if (single) return kSingle;
