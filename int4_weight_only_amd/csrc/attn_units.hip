@@ -750,6 +750,7 @@ __global__ void __launch_bounds__(256) attn_units_join_kernel(UnitArgs s) {
         l = l * f + l1 * f1;
         v = v * f + v1 * f1;
     };
+    // (Eight at once: 4 sequences over 1000 keys 17.5 us for 16.4; two: 16 over 16384 32.5 for 31.3.)
 #pragma unroll 4
     for (int i = lane / LANES; i < total; i += kWave / LANES) {
         const bool second = i >= own_parts;
