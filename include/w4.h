@@ -540,9 +540,10 @@ size_t w4_attn_cross_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cache
  * taken and returned again), after a call in which a sequence ended, or with pages put into the ring
  * behind its last one and `count` raised.  So a caller that may run out keeps them: an output in place
  * overwrites them.  Entries past the table's last column are neither written nor counted; rows there get
- * slot -1.
+ * slot -1, while lengths and positions count on, up to 2^31 - 1.
+ *   kv_len       int32 [n_seqs], values below 0 count as 0;  kv_len_out  int32 [n_seqs]
  *   n_new        int32 [n_seqs], values up to 2^30 - 1;  spans, spans_out  int32 [n_seqs][2]
- *   kv_len, kv_len_out  int32 [n_seqs];   ring_state, ring_state_out  int32 [3]
+ *   ring_state, ring_state_out  int32 [3]
  *   page_table   int32 [n_seqs][ld_table], table_cols entries used, in and out
  *   page_size    a power of two, 1 .. 32768;  table_cols * page_size and n_seqs * table_cols up to 2^30
  *   ring         int32 [ring_size], in and out.  Pages beyond its size are dropped

@@ -40,9 +40,8 @@ struct Request {
 __device__ __forceinline__ Request request(const TablesArgs &a, int b) {
     Request r;
     const int n = a.kv_len[b], m = a.n_new[b];
-    const int capacity = a.table_cols << a.page_shift;
     r.over = m < 0;
-    r.len = min(max(n, 0), capacity);
+    r.len = max(n, 0);  // (past the table's last column too: only what names pages ends there)
     r.tokens = min(max(m, 0), kMostTokens);
     r.begin = min(max(a.spans[2 * b], 0), a.table_cols);
     r.end = min(max(a.spans[2 * b + 1], r.begin), a.table_cols);
@@ -50,6 +49,10 @@ __device__ __forceinline__ Request request(const TablesArgs &a, int b) {
     r.want = static_cast<int>(
         min((keys + (1 << a.page_shift) - 1) >> a.page_shift, static_cast<int64_t>(a.table_cols)));
     return r;
+}
+
+__device__ __forceinline__ int upto_31_bits(uint32_t v) {
+    return static_cast<int>(min(v, uint32_t{INT32_MAX}));
 }
 
 // Sums over lanes 0 .. own lane; `rows` stop at T (as good as a sum: all are >= 0).
@@ -134,7 +137,8 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(TablesArgs a, in
                 if (lengths) {
                     const int got = min(max(count - first, 0), r[i].fresh());
                     a.q_start[b + 1] = at.rows;
-                    a.kv_len_out[b] = r[i].over ? 0 : r[i].len + r[i].tokens;
+                    a.kv_len_out[b] =
+                        r[i].over ? 0 : upto_31_bits(uint32_t(r[i].len) + uint32_t(r[i].tokens));
                     a.spans_out[2 * b] = r[i].over ? 0 : r[i].begin;
                     a.spans_out[2 * b + 1] = r[i].over ? 0 : r[i].end + got;
                 }
@@ -184,15 +188,18 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(TablesArgs a, in
 #pragma unroll
                 for (int i = 0; i < kAtOnce; ++i) {
                     const int b = base + p[i], end = s_end[p[i]], in = k[i] - first[i][p[i]];
+                    // (positions need 32 bits; a column beyond the table is only compared)
+                    const uint32_t pos = static_cast<uint32_t>(s_len[p[i]]) + in;
                     const int col = kind[i] == 1 ? s_begin[p[i]] + in
-                                                 : (s_len[p[i]] + in) >> a.page_shift;
+                                                 : upto_31_bits(pos >> a.page_shift);
+                    const bool inside = col < a.table_cols;
                     // number among the pages given out, of a new entry or a row on one
-                    const int number = kind[i] == 0 ? k[i] : s_fresh[p[i]] + col - end;
+                    const int number = kind[i] == 0 ? k[i] : s_fresh[p[i]] + (inside ? col - end : 0);
                     const bool held = kind[i] == 1 || (kind[i] == 2 && col < end);
                     page[i] = -1;
                     if (held)
                         page[i] = a.page_table[b * a.ld_table + col];
-                    else if (number < count && (kind[i] == 0 || col < a.table_cols))
+                    else if (number < count && (kind[i] == 0 || inside))
                         page[i] = a.ring[place_of(number)];
                 }
 #pragma unroll
@@ -204,14 +211,14 @@ __global__ void __launch_bounds__(kThreads) batch_tables_kernel(TablesArgs a, in
                     } else if (kind[i] == 1) {
                         a.ring[place_of(static_cast<int64_t>(count) + k[i])] = page[i];
                     } else {
-                        const int pos = s_len[p[i]] + in;
+                        const uint32_t pos = static_cast<uint32_t>(s_len[p[i]]) + in;
                         if (a.slots)
                             a.slots[k[i]] = page[i] < 0
                                                 ? -1
                                                 : (static_cast<int64_t>(page[i]) << a.page_shift) +
-                                                      (pos & ((1 << a.page_shift) - 1));
+                                                      (pos & ((1u << a.page_shift) - 1));
                         if (a.seqs) a.seqs[k[i]] = b;
-                        if (a.positions) a.positions[k[i]] = pos;
+                        if (a.positions) a.positions[k[i]] = upto_31_bits(pos);
                     }
                 }
             }
