@@ -484,10 +484,11 @@ size_t w4_attn_prefill_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cac
  * The other arguments are those of w4_attn_prefill.  Limits (W4_ERR_RANGE): T <= 2^21, n_seqs
  * <= 2^16, T * n_heads < 2^26, table_cols * page_size of either table up to 2^26, and n_kv_heads (T G / 64
  * + n_seqs + n_prefixes) times the 32-key tiles that either table's pages can hold below 2^29, for G =
- * n_heads / n_kv_heads.  The softmax weights enter the second product as bf16 (up to 16 rows over the same
- * keys: as two bf16 values), their sum in fp32; partial results are fp32 in `work`, joined in a fixed
- * order.  work: 8 (head_dim + 4) bytes for each row and query head, and 1024 (head_dim + 2) for each
- * compute unit.
+ * n_heads / n_kv_heads.  The softmax weights enter the second product as bf16, or as two bf16 values where
+ * head_dim is up to 128 and a key-value head has up to 16 rows (tokens times G) over the same prefix or of
+ * one sequence; their sum in fp32.  (So above 128 dims single tokens have weights within 2^-8 of
+ * themselves here, 2^-16 in w4_attn_decode.)  Partial results are fp32 in `work`, joined in a fixed order.
+ * work: 8 (head_dim + 4) bytes for each row and query head, and 1024 (head_dim + 2) for each compute unit.
  */
 typedef struct w4_prefixes {
     const int32_t *prefix_of, *table, *len;
@@ -512,6 +513,8 @@ size_t w4_attn_shared_work_bytes(int64_t T, int n_heads, const w4_kv_cache *cach
  *   cache    keys and values of the encoder's states; a dense [n_seqs][length][n_kv_heads][head_dim]
  *            is a cache of pages in ascending order
  *   the other arguments as for w4_attn_prefill.  A sequence without states gives y = 0, lse = -inf.
+ * The weights of the second product are within 2^-16 of themselves without q_start; with it they are those
+ * of w4_attn_shared where T n_heads / n_kv_heads <= 16 n_seqs, else those of w4_attn_prefill.
  * Limits (W4_ERR_RANGE): those of w4_attn_decode without q_start, else those of w4_attn_prefill.
  */
 int w4_attn_cross(const uint16_t *q, int64_t T, int64_t ldq, int n_heads, const int32_t *q_start,

@@ -1,9 +1,12 @@
-"""Batches past 256 sequences in the operators that share and cross-read a paged cache, against the plain
-implementations (tests/cache_reference.py)."""
+"""Batches past 256 sequences and the precision of the weights in the operators that share and cross-read
+a paged cache, against the plain implementations (tests/cache_reference.py)."""
 import numpy as np
 import pytest
 
+from tests import cache_reference as plain
+from tests import layer_reference as ref
 from tests.test_gpu_cache import crossed, share
+from tests.test_gpu_layer import close, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +50,40 @@ def test_cross_past_256_sequences(B, H, n_kv, D, page):
     nq[31::120] = 40 // G
     assert nq.sum() * G <= 16 * B
     crossed(rng, lens.tolist(), nq.tolist(), H, n_kv, D, page, extra=1)
+
+
+# -------------------------------------------------------------------------------------- precision
+
+
+def check_weights(batch, q, q_start, y, H, scale, cross):
+    """y (fp32) held to weights of 16 bits: two bf16 parts, each off by at most 2^-8 of what it rounds."""
+    n, D = q.shape[0], batch.D
+    wy, _, a, ds, count = plain.attention(f64(q).reshape(n, -1), f64(batch.k), f64(batch.v), batch.at,
+                                          batch.lens, q_start, H, float(np.float32(scale)), 0, 0, cross)
+    close(y.reshape(n, H, D), wy, ref.attention_bound(a, ds, count, 16), "y")
+
+
+@pytest.mark.parametrize("H,n_kv,D", [(8, 2, 64), (4, 1, 128), (4, 4, 80), (16, 1, 128), (5, 5, 8)])
+def test_shared_weights_of_few_rows(H, n_kv, D):
+    """Up to 16 rows over a prefix and of a sequence, up to 128 dims: weights as two bf16 values."""
+    rng = np.random.default_rng([62, D])
+    G = H // n_kv
+    n = 16 // G
+    prefix_len = [700, 333]
+    of = ([0] * n + [1] * n + [-1])
+    lens = [int(x) for x in rng.integers(1, 400, len(of))]
+    lens = [x + (prefix_len[g] if g >= 0 else 0) for x, g in zip(lens, of)]
+    for nq in (None, [n // 2 + 1] + [0] * (n - 1) + [1] * n + [n]):
+        q_start = np.concatenate([[0], np.cumsum([1] * len(of) if nq is None else nq)])
+        batch, q, _, y = share(rng, prefix_len, of, lens, nq, H, n_kv, D, 16)
+        check_weights(batch, q, q_start, y, H, D ** -0.5, False)
+
+
+@pytest.mark.parametrize("H,n_kv,D", [(20, 20, 64), (4, 1, 128), (8, 2, 80)])
+def test_cross_weights_of_few_rows(H, n_kv, D):
+    rng = np.random.default_rng([63, D])
+    n = 16 // (H // n_kv)
+    nq = [n, 1, 0, n // 2, 2]
+    lens = [1500, 33, 70, 900, 1]
+    batch, q, _, y = crossed(rng, lens, nq, H, n_kv, D, 16)
+    check_weights(batch, q, np.concatenate([[0], np.cumsum(nq)]), y, H, D ** -0.5, True)
