@@ -79,6 +79,7 @@ class SharedCache:
         self.ring = torch.arange(pages, dtype=torch.int32, device=device)
         self.state = ints(3)
         self.state[1] = pages
+        self.missing = ints(1)
         self.prefix_of = torch.full((n + 1,), -1, dtype=torch.int32, device=device)
         self.prefix_len = ints(1)
         size = (shape.layers, pages, shape.page_size, shape.kv_heads, shape.head_dim)
@@ -90,9 +91,17 @@ class SharedCache:
 
     def advance(self, n_new, T):
         """Pages for n_new[b] tokens of each sequence, T in all (-1: the sequence ends and its pages
-        are free again); returns where each sequence's rows begin."""
-        return w4.w4_batch_tables(self.kv_len, n_new, self.spans, self.table, self.shape.page_size,
-                                  self.ring, self.state, T, in_place=True)[0]
+        are free again); returns where each sequence's rows begin. Where the pool runs dry, keys of the
+        pass have no place, and it cannot be made again: its lengths are changed in place. See check."""
+        starts = w4.w4_batch_tables(self.kv_len, n_new, self.spans, self.table, self.shape.page_size,
+                                    self.ring, self.state, T, in_place=True)[0]
+        self.missing += self.state[2:]
+        return starts
+
+    def check(self):
+        """Raises if any pass so far, replayed ones among them, ran out of pages. Waits for the GPU."""
+        if self.missing.item() > 0:
+            raise RuntimeError(f"the pool of {self.ring.shape[0]} pages is too small: results are wrong")
 
     def share(self, b):
         """Sequence b begins after the system prompt."""
@@ -249,6 +258,8 @@ def main(argv=None):
         graph.replay()
     end.record()
     torch.cuda.synchronize()
+    if args.system > 0:
+        cache.check()
     ms = begin.elapsed_time(end) / args.steps
     print(f"{len(lens)} sequences, {args.steps} steps, {ms:.3f} ms a step "
           f"({len(lens) * 1e3 / ms:.0f} tokens/s through {args.layers} layers)", flush=True)

@@ -784,8 +784,10 @@ def w4_batch_tables(kv_len, n_new, spans, page_table, page_size, ring, ring_stat
 
     Returns (q_start int32 [n_seqs + 1], slots int64 [T], seqs int32 [T], positions int32 [T],
     kv_len, spans, ring_state), the last three new tensors, or with in_place those given.  Where
-    ring_state[2] is above 0 after the call, that many pages were missing: the step can be made again
-    from the kv_len, spans and ring_state that it had, once there are more."""
+    ring_state[2] is above 0 after the call, that many pages were missing: rows without one have slot
+    -1, their keys are not kept, and attention reads others in their place.  The step can be made again
+    from the kv_len, spans and ring_state that it had, once there are more pages; in_place overwrites
+    those, so that a caller who may run out keeps copies or does without it."""
     arrays = (kv_len, n_new, spans, page_table, ring, ring_state)
     dev = kv_len.device
     if not (kv_len.dtype is n_new.dtype is spans.dtype is page_table.dtype is ring.dtype
