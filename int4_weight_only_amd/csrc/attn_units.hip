@@ -6,7 +6,9 @@
 // not once per sequence. Work is cut into units of stacked rows of one key-value head:
 //   prefix units: rows of all sequences over prefix g, its keys
 //   own units:    rows of one sequence, its own keys; of a sequence that fills a wide unit by itself (or
-//                 has no prefix) all of its keys, by both tables: nothing is gained by sharing there
+//                 has no prefix) all of its keys, by both tables. (Such sequences share nothing, and the
+//                 rows past their last full unit take one for themselves: 64 of 18 tokens after 8000
+//                 shared keys, 28 heads over 4 of 128, 177 us, of 19 tokens, 133 rows, 238.)
 // The unit of a prefix or sequence with up to 16 rows is narrow, a wave's work (attn_narrow.h: bound by
 // reading keys), others are wide, 128 rows each, a workgroup's (attn_tile.h: bound by the products).
 //
@@ -51,7 +53,7 @@ constexpr int kTileCost = 2, kWideStart = 10, kNarrowStart = 3;
 // the products of 128 rows and the keys of a tile. (A quarter: four waves. Half of it: 256 sequences over
 // 32768 keys 182 us for 154; twice: five prefixes of up to 8000 85 us for 73.)
 template <int DP>
-constexpr float kNarrowWeight = DP > 128 ? 0.6f : DP > 64 ? 0.4f : 0.25f;
+constexpr float kNarrowWeight = DP > 64 ? 0.4f : 0.25f;
 // The shortest pieces, without a unit's start: workers that share less than this are better fewer. (A
 // piece that may have one inside is longer by it, so that none is without tiles. Wide: 8 tiles 24 us for
 // 17 with 4 sequences over 1000 keys, 2 tiles 35 for 31 with 16 over 16384. Narrow: one tile 31 us for 24,

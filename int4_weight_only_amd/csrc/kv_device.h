@@ -63,13 +63,6 @@ __device__ __forceinline__ int prefix_length(const Prefixes &x, int g) {
     const int n = read_const(x.len + g);
     return n < 0 ? 0 : (n > x.capacity ? x.capacity : n);
 }
-// Positions of sequence b that lie in its prefix, and that prefix's table row (as it was without one).
-__device__ __forceinline__ int prefix_of_seq(const Prefixes &x, int b, const int32_t **row) {
-    const int g = read_const(x.of + b);
-    if (g < 0 || g >= x.n) return 0;
-    *row = x.table + g * x.ld_table;
-    return prefix_length(x, g);
-}
 
 // Where token row t stands: its sequence, that sequence's keys, and its position (below 0: it sees
 // no key). False for a row that q_start gives to no sequence. Without q_start each sequence has
