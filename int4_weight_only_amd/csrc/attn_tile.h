@@ -738,12 +738,18 @@ void launch_tiles(const typename Rows::Args &args, int64_t blocks, hipStream_t s
 template <class Rows>
 void launch_tiles(const typename Rows::Args &args, int64_t blocks, hipStream_t stream) {
     // At 64 dims registers do for three workgroups on a compute unit (those of the second pass are
-    // spilled: with one infinity in the values 3 x 4096 523 us for 467, 8 x 1024, 20 heads, 104 for 81): prompts of 3 x 4096, 28 heads over 4, 179 to 186 us for 194 to 199; 8 x 448 rows over
-    // 1500 states, 20 heads, 49 for 55, as 580 workgroups then run at once. Where two on each hold all,
-    // three only share them out unevenly: 4 x 200 after 3000 keys 28.3 us for 27.3. (Pages under 8 slots
-    // lose where there are hardly more: 9 x 1000, 8 heads, 552 workgroups, pages of 4, 24.4 for 22.9; 8 x
-    // 1024, 20 heads, 43.5 for 47.7.)
-    if (args.c.head_dim <= 64 && blocks > 2 * int64_t{device_cu_count()})
+    // spilled: with one infinity in the values 3 x 4096, 28 heads over 4, 523 us for 467, 8 x 1024, 20
+    // heads, 104 for 81): prompts of 3 x 4096 179 to 186 us for 194 to 199; 8 x 448 rows over 1500 states,
+    // 20 heads, 49 for 55, as 580 workgroups then run at once. Where two on each hold all, three only
+    // share them out unevenly: 4 x 200 after 3000 keys 28.3 us for 27.3.
+    // Pages under 8 slots, whose rows each have an address, take longer side by side: where most rows see
+    // all keys before them, three gain with more than four for each only (pages of 4, 8 heads, us for
+    // three / two: one prompt of 11000, 688 workgroups, 230 / 200, of 12500, 784, 266 / 228, of 16000,
+    // 1008, 350 / 382; 8 x 1024, 20 heads, 1280, 43.5 / 47.7; window 4096, one of 9000, 568, 105 / 98),
+    // within windows as elsewhere (2 x 5000, 576, window 512, 26.8 / 32.9; one of 9000, window 1024, 38.7
+    // / 46.0).
+    const bool by_rows = args.c.page_mask < 7 && !(args.a.window > 0 && args.a.window <= 1024);
+    if (args.c.head_dim <= 64 && blocks > (by_rows ? 4 : 2) * int64_t{device_cu_count()})
         launch_tiles<Rows, 64, 3>(args, blocks, stream);
     else if (args.c.head_dim <= 64)
         launch_tiles<Rows, 64, 2>(args, blocks, stream);

@@ -2,11 +2,13 @@
 a paged cache, against the plain implementations (tests/cache_reference.py)."""
 import numpy as np
 import pytest
+import torch
 
+import int4_weight_only_amd as w4
 from tests import cache_reference as plain
 from tests import layer_reference as ref
-from tests.test_gpu_cache import crossed, share
-from tests.test_gpu_layer import close, f64
+from tests.test_gpu_cache import MANY_KEYS, MANY_ROWS, Batch, crossed, ints, seen_slots, share
+from tests.test_gpu_layer import bf16, close, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -50,6 +52,35 @@ def test_cross_past_256_sequences(B, H, n_kv, D, page):
     nq[31::120] = 40 // G
     assert nq.sum() * G <= 16 * B
     crossed(rng, lens.tolist(), nq.tolist(), H, n_kv, D, page, extra=1)
+
+
+@pytest.mark.parametrize("page", [1, 4])
+@pytest.mark.parametrize("form,H", [("cross", 34), ("prefill", 34), ("window", 17)])
+def test_many_rows_on_small_pages(form, H, page):
+    """Workgroups of 64 dims on pages under 8 slots, many enough to run three on a compute unit (with a
+    window fewer do), against calls of one sequence, bit for bit."""
+    rng = np.random.default_rng([64, page])
+    # (448 keys: too few to be split where a sequence is alone)
+    lens = [min(max(n, m), 448) for n, m in zip(MANY_KEYS, MANY_ROWS)]
+    rows = [min(m, n) for m, n in zip(MANY_ROWS, lens)]
+    batch = Batch(rng, [0], [-1] * len(lens), lens, page, H, 64, cols=448 // page)
+    starts = np.concatenate([[0], np.cumsum(rows)])
+    assert (starts[-1] // 128 + len(lens)) * H > (512 if form == "window" else 1024)
+    batch.fill(rng, seen_slots(batch, starts, 0, 0, True))
+    q = bf16(2.0 * rng.normal(size=(starts[-1], H * 64))).cuda()
+    k, v, table, kv_len = batch.args()
+
+    def call(q, table, kv_len, starts):
+        if form == "cross":
+            return w4.w4_attn_cross(q, k, v, table, kv_len, ints(starts), out_dtype=w4.W4_OUT_F32)
+        return w4.w4_attn_prefill(q, k, v, table, kv_len, ints(starts), out_dtype=w4.W4_OUT_F32,
+                                  window=200 if form == "window" else 0)
+    y = call(q, table, kv_len, starts)
+    assert torch.isfinite(y).all()
+    for b, n in enumerate(rows):
+        if n:
+            one = slice(int(starts[b]), int(starts[b + 1]))
+            assert torch.equal(call(q[one], table[b:b + 1], kv_len[b:b + 1], [0, n]), y[one])
 
 
 # -------------------------------------------------------------------------------------- precision
